@@ -520,6 +520,87 @@ MOE_API moe_status moe_ep_experts(const void* recv, const int32_t* counts_all, i
 MOE_API moe_status moe_ep_combine(const float* ysend, const float* topk_w, const int32_t* send_pos, int T, int d,
                                   int k, void* out, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Grouped products by expert with ragged rows: the matrix products under the
+ * layer's experts (subsection "各エキスパートの構造": W1 x, W3 x and W2 h per
+ * expert) on their own, with both gradients, for callers that build other
+ * experts around the router and the dispatch.
+ *
+ *   moe_grouped_mm     y_r  = W_e x_r                    rows r of segment e
+ *   moe_grouped_dgrad  dx_r = W_e^T dy_r
+ *   moe_grouped_wgrad  dW_e = sum_{r in segment e} dy_r x_r^T
+ *
+ *   x, dx [M][K]   y, dy [M][N]   W, dW [E][N][K]   (device)
+ *   offsets [E+1] int32 (device): segment e starts at row offsets[e];
+ *   counts  [E]   int32 (device) or NULL: its rows; NULL: up to offsets[e+1].
+ * Segments need no alignment, may be empty and may leave gaps (the padded
+ * segments of moe_dispatch fit: pass its counts and offsets).  Rows in no
+ * segment are not read into any result and not written; an empty segment's dW
+ * is zero.  Offsets must not decrease or leave [0, M], and a segment must end
+ * by offsets[e+1]: else MOE_ERR_DEVICE is recorded and nothing is written.
+ * Unlike in the layer calls, NaN and Inf are allowed: they reach the results
+ * that the formulas give them and no others.
+ *
+ * dtype: MOE_DTYPE_BF16 (fp32 sums; out_dtype MOE_DTYPE_BF16, rounded once, or
+ * MOE_DTYPE_F32) or MOE_DTYPE_F32 (fp32 throughout, out_dtype MOE_DTYPE_F32).
+ * The sum of one output runs in an order that depends on the sizes alone:
+ * results are bitwise repeatable.  Outputs must not overlap inputs.
+ * Sizes: E <= 256; N and K multiples of 8 (bfloat16) or 4 (float).  M == 0 is
+ * a no-op (moe_grouped_wgrad then writes zeros).  No workspace; calls can be
+ * captured into a CUDA graph after one call on the device.
+ * ------------------------------------------------------------------------ */
+MOE_API moe_status moe_grouped_mm(const void* x, const void* W, const int32_t* offsets, const int32_t* counts, void* y,
+                                  int M, int N, int K, int E, int dtype, int out_dtype, cudaStream_t stream);
+MOE_API moe_status moe_grouped_dgrad(const void* dy, const void* W, const int32_t* offsets, const int32_t* counts,
+                                     void* dx, int M, int N, int K, int E, int dtype, int out_dtype,
+                                     cudaStream_t stream);
+MOE_API moe_status moe_grouped_wgrad(const void* dy, const void* x, const int32_t* offsets, const int32_t* counts,
+                                     void* dW, int M, int N, int K, int E, int dtype, int out_dtype,
+                                     cudaStream_t stream);
+
+/*
+ * moe_grouped_mm with low-rank adapters of many requests at once (bfloat16):
+ *   y_r = W_e x_r + B_{a,e} (s_a A_{a,e} x_r),   a = adapter[r]
+ *   A [L][E][R][K], B [L][E][N][R] bf16, scale [L] float, adapter [M] int32
+ *   (device): the row's adapter in [0, L), or -1 for none.  Rows of one adapter
+ *   need not be neighbours.  E = 1 with offsets {0, M}: one shared projection.
+ * s_a A x is rounded once to bf16 (the second product's operand type); the sum
+ * of both products is rounded once.  An id outside [-1, L) in a segment records
+ * MOE_ERR_DEVICE.  Sizes: as moe_grouped_mm; R a multiple of 8, at most
+ * MOE_LORA_MAX_RANK.  workspace: moe_grouped_lora_workspace_size() bytes
+ * (device, 256-byte aligned, not in use by another call in flight).
+ */
+enum { MOE_LORA_MAX_RANK = 128 };
+MOE_API size_t moe_grouped_lora_workspace_size(int M, int E, int L, int R);
+MOE_API moe_status moe_grouped_lora(const void* x, const void* W, const int32_t* offsets, const int32_t* counts,
+                                    const void* A, const void* B, const float* scale, const int32_t* adapter, void* y,
+                                    int M, int N, int K, int E, int L, int R, int out_dtype, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The global norm of a list of gradients, and clipping by it (for the gradients
+ * of moe_backward_ws and moe_block_backward_ws, or any others):
+ *   n = sqrt(sum_i sum_j g_ij^2),   out_ij = g_ij c,   c = min(1, max_norm / (n + eps))
+ * grads, out: arrays of `count` descriptors (host; read during the call) of
+ * device tensors, contiguous, bfloat16 or float, mixed freely, any length, data
+ * aligned to their element.  out NULL: in place (nothing is written when
+ * c = 1); else out[i] has grads[i]'s length and type, and may be grads[i]
+ * itself but no output may overlap another tensor.  norm [1] float (device,
+ * out): n.  Squares are summed in fp64 over fp32 sums of at most 32, in a fixed
+ * order (bitwise repeatable).  A NaN in any gradient makes n and every output
+ * NaN; an infinite n gives c = 0.  0 <= max_norm <= Inf, 0 <= eps < Inf.
+ * Scratch comes from the library's stream-ordered pool.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    void* data;
+    int64_t numel;
+    int32_t dtype; /* MOE_DTYPE_* */
+} moe_tensor;
+
+MOE_API moe_status moe_grad_norm(const moe_tensor* grads, int count, float* norm, cudaStream_t stream);
+MOE_API moe_status moe_clip_grads(const moe_tensor* grads, const moe_tensor* out, int count, float max_norm, float eps,
+                                  float* norm, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,7 +11,9 @@ bf16 tensors are torch.bfloat16; the layer's operand layouts are
     x [T][d], Wg [E][d], W1 [E][F][d], W3 [E][F][d], W2 [E][d][F], out [T][d].
 The block form adds h [T][d] (the residual stream, in place of x) and
 gamma [d]; load-balance statistics come back as a float32 [2E+1] tensor
-(f, p, loss).
+(f, p, loss).  The grouped products (moe_grouped_*) take the experts' weights on
+their own, with rows in any segments; moe_grad_norm and moe_clip_grads take the
+gradients of the backward calls.
 """
 from __future__ import annotations
 
@@ -82,6 +84,13 @@ SIGNATURES = {
     "moe_ep_dispatch": (_ci, [_vp, _vp, _ci, _ci, _ci, _ci, _vp, _vp, _vp, _vp]),
     "moe_ep_experts": (_ci, [_vp, _vp, _ci, _ci, _ci, _vp, _vp, _vp, _ci, _ci, _vp, _vp]),
     "moe_ep_combine": (_ci, [_vp, _vp, _vp, _ci, _ci, _ci, _vp, _vp]),
+    "moe_grouped_mm": (_ci, [_vp] * 5 + [_ci] * 6 + [_vp]),
+    "moe_grouped_dgrad": (_ci, [_vp] * 5 + [_ci] * 6 + [_vp]),
+    "moe_grouped_wgrad": (_ci, [_vp] * 5 + [_ci] * 6 + [_vp]),
+    "moe_grouped_lora_workspace_size": (_sz, [_ci] * 4),
+    "moe_grouped_lora": (_ci, [_vp] * 9 + [_ci] * 7 + [_vp, _sz, _vp]),
+    "moe_grad_norm": (_ci, [_vp, _ci, _vp, _vp]),
+    "moe_clip_grads": (_ci, [_vp, _vp, _ci, _cf, _cf, _vp, _vp]),
 }
 for _name, (_res, _args) in SIGNATURES.items():
     _f = getattr(_lib, _name)
@@ -579,6 +588,169 @@ def moe_ep_combine(ysend, topk_w, send_pos, out=None, stream=None):
     _check(_lib.moe_ep_combine(_ptr(ysend), _ptr(topk_w), _ptr(send_pos), T, d, k, _ptr(out),
                                _stream(stream, ysend, topk_w, send_pos, out)), "moe_ep_combine")
     return out
+
+
+def _segment_args(offsets, counts):
+    """offsets int32 [E+1] and counts int32 [E] or None: E."""
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must be a 1-D tensor of E + 1 values")
+    E = offsets.numel() - 1
+    if counts is not None and (not isinstance(counts, torch.Tensor) or counts.shape != (E,)):
+        raise ValueError(f"counts must be a 1-D tensor of {E} values")
+    _dev(offsets, torch.int32, "offsets")
+    if counts is not None:
+        _dev(counts, torch.int32, "counts")
+    return E
+
+
+def _grouped_out(out, shape, dtype, like):
+    """The output tensor of a grouped product: the caller's, of exactly `shape` (rows in no segment keep
+    what it holds), or a new one."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+    if not isinstance(out, torch.Tensor) or tuple(out.shape) != tuple(shape):
+        raise ValueError(f"out must have shape {tuple(shape)}")
+    if dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out must be {dtype}, got {out.dtype}")
+    return out
+
+
+def _grouped(name, a, b, a_name, b_name, offsets, counts, out, M, N, K, E, stream):
+    code = _dtype_code(a)
+    _dev(a, a.dtype, a_name)
+    _dev(b, a.dtype, b_name)
+    ocode = _dtype_code(out)
+    _dev(out, out.dtype, "out")
+    _check(getattr(_lib, name)(_ptr(a), _ptr(b), _ptr(offsets), _ptr(counts), _ptr(out), M, N, K, E, code, ocode,
+                               _stream(stream, a, b, offsets, counts, out)), name)
+    return out
+
+
+def moe_grouped_mm(x, W, offsets, counts=None, out=None, out_dtype=None, stream=None):
+    """y_r = W_e x_r for the rows r of every expert e's segment: x [M][K], W [E][N][K], y [M][N].
+    Segment e is rows [offsets[e], offsets[e] + counts[e]), or up to offsets[e+1] without counts (int32
+    CUDA tensors; moe_dispatch's fit).  Rows in no segment are not written.  bf16 inputs give bf16, or
+    float32 with out_dtype=torch.float32; float32 inputs float32."""
+    E = _segment_args(offsets, counts)
+    if x.dim() != 2 or W.dim() != 3 or W.shape[0] != E or W.shape[2] != x.shape[1]:
+        raise ValueError(f"inconsistent shapes x{tuple(x.shape)} W{tuple(W.shape)} for {E} segments")
+    (M, K), N = x.shape, W.shape[1]
+    out = _grouped_out(out, (M, N), out_dtype, x)
+    return _grouped("moe_grouped_mm", x, W, "x", "W", offsets, counts, out, M, N, K, E, stream)
+
+
+def moe_grouped_dgrad(dy, W, offsets, counts=None, out=None, out_dtype=None, stream=None):
+    """dx_r = W_e^T dy_r, the rows' gradient of moe_grouped_mm: dy [M][N], W [E][N][K], dx [M][K]."""
+    E = _segment_args(offsets, counts)
+    if dy.dim() != 2 or W.dim() != 3 or W.shape[0] != E or W.shape[1] != dy.shape[1]:
+        raise ValueError(f"inconsistent shapes dy{tuple(dy.shape)} W{tuple(W.shape)} for {E} segments")
+    (M, N), K = dy.shape, W.shape[2]
+    out = _grouped_out(out, (M, K), out_dtype, dy)
+    return _grouped("moe_grouped_dgrad", dy, W, "dy", "W", offsets, counts, out, M, N, K, E, stream)
+
+
+def moe_grouped_wgrad(dy, x, offsets, counts=None, out=None, out_dtype=None, stream=None):
+    """dW_e = sum over segment e's rows of dy_r x_r^T, the weights' gradient of moe_grouped_mm: dy [M][N],
+    x [M][K], dW [E][N][K] (zero for an empty segment)."""
+    E = _segment_args(offsets, counts)
+    if dy.dim() != 2 or x.dim() != 2 or x.shape[0] != dy.shape[0]:
+        raise ValueError(f"inconsistent shapes dy{tuple(dy.shape)} x{tuple(x.shape)}")
+    (M, N), K = dy.shape, x.shape[1]
+    out = _grouped_out(out, (E, N, K), out_dtype, dy)
+    return _grouped("moe_grouped_wgrad", dy, x, "dy", "x", offsets, counts, out, M, N, K, E, stream)
+
+
+def moe_grouped_lora_workspace_size(M, E, L, R) -> int:
+    return int(_lib.moe_grouped_lora_workspace_size(M, E, L, R))
+
+
+def moe_grouped_lora(x, W, offsets, A, B, scale, adapter, counts=None, out=None, out_dtype=None, workspace=None,
+                     stream=None):
+    """moe_grouped_mm with low-rank adapters (bf16): y_r = W_e x_r + B[a, e] (scale[a] A[a, e] x_r) with
+    a = adapter[r] (int32 [M], -1: none); A [L][E][R][K], B [L][E][N][R], scale float32 [L].  With one
+    expert (offsets [0, M]) it is one shared projection beside the adapters of a mixed batch."""
+    E = _segment_args(offsets, counts)
+    if x.dim() != 2 or W.dim() != 3 or W.shape[0] != E or W.shape[2] != x.shape[1]:
+        raise ValueError(f"inconsistent shapes x{tuple(x.shape)} W{tuple(W.shape)} for {E} segments")
+    (M, K), N = x.shape, W.shape[1]
+    if A.dim() != 4 or B.dim() != 4 or A.shape[1] != E or A.shape[3] != K or \
+            tuple(B.shape) != (A.shape[0], E, N, A.shape[2]):
+        raise ValueError(f"inconsistent adapter shapes A{tuple(A.shape)} B{tuple(B.shape)}")
+    L, R = A.shape[0], A.shape[2]
+    if scale.shape != (L,) or adapter.shape != (M,):
+        raise ValueError(f"scale must have shape ({L},) and adapter ({M},)")
+    for t, n in ((x, "x"), (W, "W"), (A, "A"), (B, "B")):
+        _dev(t, torch.bfloat16, n)
+    _dev(scale, torch.float32, "scale")
+    _dev(adapter, torch.int32, "adapter")
+    out = _grouped_out(out, (M, N), out_dtype, x)
+    ocode = _dtype_code(out)
+    _dev(out, out.dtype, "out")
+    if workspace is None:
+        workspace = torch.empty(max(moe_grouped_lora_workspace_size(M, E, L, R), 1), dtype=torch.uint8,
+                                device=x.device)
+    _dev(workspace, torch.uint8, "workspace")
+    _check(_lib.moe_grouped_lora(_ptr(x), _ptr(W), _ptr(offsets), _ptr(counts), _ptr(A), _ptr(B), _ptr(scale),
+                                 _ptr(adapter), _ptr(out), M, N, K, E, L, R, ocode, _ptr(workspace),
+                                 workspace.numel(),
+                                 _stream(stream, x, W, offsets, counts, A, B, scale, adapter, out, workspace)),
+           "moe_grouped_lora")
+    return out
+
+
+class _MoETensor(ctypes.Structure):
+    _fields_ = [("data", _vp), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+def _tensor_list(tensors, name):
+    arr = (_MoETensor * max(len(tensors), 1))()
+    for d, t in zip(arr, tensors):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be CUDA tensors")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        d.data, d.numel, d.dtype = t.data_ptr(), t.numel(), _dtype_code(t)
+    return arr
+
+
+def _grad_list(grads):
+    """The gradients of a call: a list, or the dict that a backward returns; None entries are left out."""
+    return [g for g in (grads.values() if isinstance(grads, dict) else grads) if g is not None]
+
+
+def _norm_tensor(norm, grads):
+    if norm is None:
+        if not grads:
+            raise ValueError("an empty list of gradients needs norm=")
+        norm = torch.empty(1, dtype=torch.float32, device=grads[0].device)
+    _room(norm, 1, "norm")
+    return _dev(norm, torch.float32, "norm")
+
+
+def moe_grad_norm(grads, norm=None, stream=None):
+    """The global 2-norm of a list (or dict) of gradients, bf16 and float32 mixed: float32 [1] on the device."""
+    grads = _grad_list(grads)
+    arr = _tensor_list(grads, "grads")
+    norm = _norm_tensor(norm, grads)
+    _check(_lib.moe_grad_norm(arr, len(grads), _ptr(norm), _stream(stream, norm, *grads)), "moe_grad_norm")
+    return norm
+
+
+def moe_clip_grads(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
+    """Scale every gradient by min(1, max_norm / (n + eps)), n the global 2-norm: in place, or into the
+    tensors of `out` (same shapes and types).  Returns (norm float32 [1], the list of clipped tensors).
+    No host synchronisation."""
+    grads = _grad_list(grads)
+    outs = grads if out is None else _grad_list(out)
+    if len(outs) != len(grads) or any(o.shape != g.shape or o.dtype != g.dtype for o, g in zip(outs, grads)):
+        raise ValueError("out must match the gradients in number, shape and dtype")
+    arr = _tensor_list(grads, "grads")
+    oarr = None if out is None else _tensor_list(outs, "out")
+    norm = _norm_tensor(norm, grads)
+    tensors = grads if out is None else grads + outs
+    _check(_lib.moe_clip_grads(arr, oarr, len(grads), float(max_norm), float(eps), _ptr(norm),
+                               _stream(stream, norm, *tensors)), "moe_clip_grads")
+    return norm, outs
 
 
 def moe_get_device_status(stream=None) -> int:

@@ -1,0 +1,388 @@
+// The global norm of a list of gradient tensors, and clipping by it:
+//     n = sqrt(sum_i sum_j g_ij^2),   out_ij = g_ij min(1, max_norm / (n + eps)).
+//
+// Both passes are bound by HBM.  The list is cut into chunks of kChunk elements
+// (no chunk spans two tensors) and every block takes one contiguous run of them.
+// Pass 1 squares and sums: a thread adds the squares of up to 32 values in fp32
+// and adds that sum to its total in fp64, so neither the length of the list nor
+// the order of the chunks costs digits; where the fp32 sum leaves the range in
+// which it is good (values near 1e-14 or 1e19 and beyond) it is taken again in fp64.
+// Each block writes one fp64 partial sum, and pass 2's blocks each add all of
+// them in the same fixed order: no atomics, the same bits on every run.
+// Pass 2 scales.  It walks every block's run backwards, so that it starts with
+// what pass 1 read last and still finds it in L2.
+#include <algorithm>
+#include <vector>
+
+#include "moe_common.cuh"
+
+namespace moe {
+int* status_word(int dev);
+cudaMemPool_t library_pool(int dev);
+int device_sms(int dev);
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunk = 8192;            // elements
+constexpr int kBlocksPerSm = 4;
+constexpr int kMaxTensors = 256;        // of one launch (they travel as kernel parameters)
+constexpr int kMaxPartials = 8192;      // pass 2 adds them all in every block
+
+struct Entry {
+    const void* g;
+    void* out;
+    long long n;
+    int is16;
+    int vec;   // both pointers 16-byte aligned
+};
+
+template <int CAP>
+struct List {
+    Entry t[CAP];
+    long long chunk0[CAP + 1];   // first chunk of each tensor
+    int count;
+};
+
+// Visit this block's chunks: f(entry, first element, elements).
+template <int CAP, bool BACKWARD, typename F>
+__device__ __forceinline__ void for_chunks(const List<CAP>& l, F&& f) {
+    const long long total = l.chunk0[l.count];
+    const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+    if (lo >= hi) return;
+    const long long first = BACKWARD ? hi - 1 : lo;
+    int a = 0, b = l.count;   // chunk0[a] <= first < chunk0[b]
+    while (b - a > 1) {
+        const int m = (a + b) >> 1;
+        if (l.chunk0[m] <= first) a = m;
+        else b = m;
+    }
+    for (long long c = first; BACKWARD ? c >= lo : c < hi; BACKWARD ? --c : ++c) {
+        while (c < l.chunk0[a]) --a;
+        while (c >= l.chunk0[a + 1]) ++a;
+        const long long e0 = (c - l.chunk0[a]) * kChunk;
+        const long long n = l.t[a].n - e0;
+        f(l.t[a], e0, n < kChunk ? (int)n : kChunk);
+    }
+}
+
+// 16 bytes as floats: 8 bf16 or 4 fp32.
+template <bool IS16>
+struct Vec {
+    static constexpr int N = IS16 ? 8 : 4;
+    float v[N];
+    __device__ __forceinline__ void set(uint4 w) {
+        const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (IS16) {
+                v[2 * i] = bf16_lo(q[i]);
+                v[(2 * i + 1) % N] = bf16_hi(q[i]);
+            } else {
+                v[i] = __uint_as_float(q[i]);
+            }
+        }
+    }
+    __device__ __forceinline__ uint4 get(float c) const {
+        uint32_t q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            q[i] = IS16 ? pack_bf16x2(v[2 * i] * c, v[(2 * i + 1) % N] * c) : __float_as_uint(v[i] * c);
+        return make_uint4(q[0], q[1], q[2], q[3]);
+    }
+};
+
+__device__ __forceinline__ float load1(const void* p, long long i, int is16) {
+    return is16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+constexpr int kUnroll = 4;   // 16-byte loads in flight per thread
+
+template <bool IS16>
+__device__ __forceinline__ double chunk_squares(const void* g, long long e0, int n) {
+    constexpr int N = Vec<IS16>::N;
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(g) + e0 * (IS16 ? 2 : 4));
+    const int nv = n / N;
+    double acc = 0.0;
+    for (int i0 = threadIdx.x; i0 < nv; i0 += kThreads * kUnroll) {
+        uint4 w[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + u * kThreads;
+            w[u] = i < nv ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            Vec<IS16> x;
+            x.set(w[u]);
+#pragma unroll
+            for (int k = 0; k < N; ++k) s = fmaf(x.v[k], x.v[k], s);
+        }
+        if (s > 1e-28f && s < 1e38f) {
+            acc += (double)s;
+        } else {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                Vec<IS16> x;
+                x.set(w[u]);
+#pragma unroll
+                for (int k = 0; k < N; ++k) acc += (double)x.v[k] * (double)x.v[k];
+            }
+        }
+    }
+    const int rest = nv * N + threadIdx.x;
+    if (rest < n) {
+        const double v = load1(g, e0 + rest, IS16);
+        acc += v * v;
+    }
+    return acc;
+}
+
+__device__ __forceinline__ double block_sum(double v, double* sh) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) s += sh[w];
+    return s;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ List<CAP> l,
+                                                             double* __restrict__ part) {
+    pdl_trigger();
+    pdl_wait();
+    __shared__ double sh[kThreads / 32];
+    double acc = 0.0;
+    for_chunks<CAP, false>(l, [&](const Entry& t, long long e0, int n) {
+        if (!t.vec) {
+            for (int i = threadIdx.x; i < n; i += kThreads) {
+                const double v = load1(t.g, e0 + i, t.is16);
+                acc += v * v;
+            }
+        } else if (t.is16) {
+            acc += chunk_squares<true>(t.g, e0, n);
+        } else {
+            acc += chunk_squares<false>(t.g, e0, n);
+        }
+    });
+    const double s = block_sum(acc, sh);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+__device__ __forceinline__ double total_norm(const double* part, int np, double* sh) {
+    double v = 0.0;
+    for (int i = threadIdx.x; i < np; i += kThreads) v += part[i];
+    return sqrt(block_sum(v, sh));
+}
+
+template <bool IS16>
+__device__ __forceinline__ void chunk_scale(const void* g, void* out, long long e0, int n, float c) {
+    constexpr int N = Vec<IS16>::N;
+    const size_t off = (size_t)e0 * (IS16 ? 2 : 4);
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(g) + off);
+    uint4* q = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + off);
+    const int nv = n / N;
+    for (int i0 = threadIdx.x; i0 < nv; i0 += kThreads * kUnroll) {
+        uint4 w[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (i0 + u * kThreads < nv) w[u] = p[i0 + u * kThreads];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (i0 + u * kThreads >= nv) continue;
+            Vec<IS16> x;
+            x.set(w[u]);
+            q[i0 + u * kThreads] = x.get(c);
+        }
+    }
+    const int rest = nv * N + threadIdx.x;
+    if (rest < n) {
+        const float v = load1(g, e0 + rest, IS16) * c;
+        if (IS16) static_cast<__nv_bfloat16*>(out)[e0 + rest] = __float2bfloat16_rn(v);
+        else static_cast<float*>(out)[e0 + rest] = v;
+    }
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) grad_clip_kernel(const __grid_constant__ List<CAP> l,
+                                                             const double* __restrict__ part, int np, float max_norm,
+                                                             float eps, float* norm) {
+    pdl_trigger();
+    pdl_wait();
+    __shared__ double sh[kThreads / 32];
+    const double nrm = total_norm(part, np, sh);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)nrm;
+    // a NaN norm fails the comparison and makes a NaN factor
+    const double t = nrm + (double)eps;
+    const float c = t <= (double)max_norm ? 1.f : (float)((double)max_norm / t);
+    for_chunks<CAP, true>(l, [&](const Entry& e, long long e0, int n) {
+        if (c == 1.f && e.out == e.g) return;   // in place and nothing to clip
+        if (!e.vec) {
+            for (int i = threadIdx.x; i < n; i += kThreads) {
+                const float v = load1(e.g, e0 + i, e.is16) * c;
+                if (e.is16) static_cast<__nv_bfloat16*>(e.out)[e0 + i] = __float2bfloat16_rn(v);
+                else static_cast<float*>(e.out)[e0 + i] = v;
+            }
+        } else if (e.is16) {
+            chunk_scale<true>(e.g, e.out, e0, n, c);
+        } else {
+            chunk_scale<false>(e.g, e.out, e0, n, c);
+        }
+    });
+}
+
+__global__ void __launch_bounds__(kThreads) norm_finish_kernel(const double* __restrict__ part, int np, float* norm) {
+    pdl_trigger();
+    pdl_wait();
+    __shared__ double sh[kThreads / 32];
+    const double nrm = total_norm(part, np, sh);
+    if (threadIdx.x == 0) *norm = (float)nrm;
+}
+
+// The launches of one call: up to kMaxTensors tensors each.
+int launches_of(int n) { return (n + kMaxTensors - 1) / kMaxTensors; }
+
+template <int CAP>
+int fill(List<CAP>* l, const moe_tensor* g, const moe_tensor* out, int n, int max_blocks) {
+    long long c = 0;
+    for (int i = 0; i < n; ++i) {
+        void* o = out ? out[i].data : g[i].data;
+        l->t[i] = {g[i].data, o, (long long)g[i].numel, g[i].dtype == MOE_DTYPE_BF16,
+                   ((reinterpret_cast<uintptr_t>(g[i].data) | reinterpret_cast<uintptr_t>(o)) & 15u) == 0};
+        l->chunk0[i] = c;
+        c += (g[i].numel + kChunk - 1) / kChunk;
+    }
+    l->chunk0[n] = c;
+    l->count = n;
+    return (int)std::max(1LL, std::min(c, (long long)max_blocks));
+}
+
+template <int CAP>
+cudaError_t norm_pass(const moe_tensor* g, int n, int max_blocks, double* part, int* blocks, cudaStream_t s) {
+    List<CAP> l;
+    *blocks = fill(&l, g, nullptr, n, max_blocks);
+    return launch_pdl(grad_norm_kernel<CAP>, dim3(*blocks), dim3(kThreads), 0, s, l, part);
+}
+
+template <int CAP>
+cudaError_t clip_pass(const moe_tensor* g, const moe_tensor* out, int n, int max_blocks, const double* part, int np,
+                      float max_norm, float eps, float* norm, cudaStream_t s) {
+    List<CAP> l;
+    const int blocks = fill(&l, g, out, n, max_blocks);
+    return launch_pdl(grad_clip_kernel<CAP>, dim3(blocks), dim3(kThreads), 0, s, l, part, np, max_norm, eps, norm);
+}
+
+moe_status check_list(const moe_tensor* t, int n) {
+    if (n < 0 || (n > 0 && !t)) return MOE_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i) {
+        if (t[i].numel < 0 || (t[i].dtype != MOE_DTYPE_BF16 && t[i].dtype != MOE_DTYPE_F32)) return MOE_ERR_INVALID_ARG;
+        if (t[i].numel > 0 && !t[i].data) return MOE_ERR_INVALID_ARG;
+        if (reinterpret_cast<uintptr_t>(t[i].data) & (t[i].dtype == MOE_DTYPE_BF16 ? 1u : 3u))
+            return MOE_ERR_INVALID_ARG;
+    }
+    return MOE_OK;
+}
+
+struct Range {
+    uintptr_t lo, hi;
+    int i;
+};
+
+Range range_of(const moe_tensor& t, int i) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(t.data);
+    return {p, p + (uintptr_t)t.numel * (t.dtype == MOE_DTYPE_BF16 ? 2 : 4), i};
+}
+
+// Outputs must not overlap one another, nor any input but their own (and that one exactly).
+bool outputs_disjoint(const moe_tensor* g, const moe_tensor* out, int n) {
+    std::vector<Range> r;
+    r.reserve(n);
+    for (int i = 0; i < n; ++i)
+        if (out[i].numel > 0) r.push_back(range_of(out[i], i));
+    std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    for (size_t i = 1; i < r.size(); ++i)
+        if (r[i].lo < r[i - 1].hi) return false;
+    if (g == out) return true;
+    for (int i = 0; i < n; ++i) {
+        if (g[i].numel == 0) continue;
+        const Range q = range_of(g[i], i);
+        auto it = std::upper_bound(r.begin(), r.end(), q.lo, [](uintptr_t v, const Range& a) { return v < a.hi; });
+        for (; it != r.end() && it->lo < q.hi; ++it)
+            if (it->i != i || it->lo != q.lo) return false;
+    }
+    return true;
+}
+
+moe_status run(const moe_tensor* g, const moe_tensor* out, int n, bool clip, float max_norm, float eps, float* norm,
+               cudaStream_t s) {
+    const DeviceScope scope(norm, true);
+    const int dev = scope.device();
+    if (dev < 0) return MOE_ERR_INVALID_ARG;
+    const cudaMemPool_t pool = library_pool(dev);
+    if (!pool) return MOE_ERR_CUDA;
+    const int sms = device_sms(dev) > 0 ? device_sms(dev) : 148;
+    const int nl = std::max(1, launches_of(n));
+    const int max_blocks = std::min(sms * kBlocksPerSm, kMaxPartials / nl);
+    if (max_blocks < 1) return MOE_ERR_UNSUPPORTED;
+    void* ws = nullptr;
+    if (cudaMallocFromPoolAsync(&ws, (size_t)nl * max_blocks * sizeof(double), pool, s) != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_WORKSPACE;
+    }
+    double* part = static_cast<double*>(ws);
+    int np = 0;
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < n && e == cudaSuccess; i += kMaxTensors) {
+        const int m = std::min(n - i, kMaxTensors);
+        int blocks = 0;
+        e = m <= 32 ? norm_pass<32>(g + i, m, max_blocks, part + np, &blocks, s)
+                    : norm_pass<kMaxTensors>(g + i, m, max_blocks, part + np, &blocks, s);
+        np += blocks;
+    }
+    if (!clip || n == 0) {
+        if (e == cudaSuccess) e = launch_pdl(norm_finish_kernel, dim3(1), dim3(kThreads), 0, s, part, np, norm);
+    } else {
+        for (int i = 0; i < n && e == cudaSuccess; i += kMaxTensors) {
+            const int m = std::min(n - i, kMaxTensors);
+            float* nm = i == 0 ? norm : nullptr;
+            e = m <= 32 ? clip_pass<32>(g + i, out + i, m, max_blocks, part, np, max_norm, eps, nm, s)
+                        : clip_pass<kMaxTensors>(g + i, out + i, m, max_blocks, part, np, max_norm, eps, nm, s);
+        }
+    }
+    const cudaError_t f = cudaFreeAsync(ws, s);
+    return e == cudaSuccess && f == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_grad_norm(const moe_tensor* grads, int n, float* norm, cudaStream_t stream) {
+    const moe_status st = check_list(grads, n);
+    if (st != MOE_OK) return st;
+    if (!norm || (reinterpret_cast<uintptr_t>(norm) & 3u)) return MOE_ERR_INVALID_ARG;
+    return run(grads, nullptr, n, false, 0.f, 0.f, norm, stream);
+}
+
+extern "C" moe_status moe_clip_grads(const moe_tensor* grads, const moe_tensor* out, int n, float max_norm, float eps,
+                                     float* norm, cudaStream_t stream) {
+    moe_status st = check_list(grads, n);
+    if (st == MOE_OK && out) st = check_list(out, n);
+    if (st != MOE_OK) return st;
+    if (!norm || (reinterpret_cast<uintptr_t>(norm) & 3u)) return MOE_ERR_INVALID_ARG;
+    if (!(max_norm >= 0.f) || !(eps >= 0.f) || !(eps <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
+    if (!out) out = grads;
+    for (int i = 0; i < n; ++i)
+        if (out[i].numel != grads[i].numel || out[i].dtype != grads[i].dtype) return MOE_ERR_INVALID_ARG;
+    try {
+        if (!outputs_disjoint(grads, out, n)) return MOE_ERR_INVALID_ARG;
+    } catch (...) {   // no host memory for the check
+        return MOE_ERR_WORKSPACE;
+    }
+    return run(grads, out, n, true, max_norm, eps, norm, stream);
+}

@@ -1,0 +1,111 @@
+// Shared by the ragged grouped products (grouped_*.cu, lora.cu): the segments of
+// the rows, their tile table, and the launcher declarations.
+//
+// Segment e holds rows [offsets[e], offsets[e] + n_e) of the row buffers, with
+// n_e = counts[e], or offsets[e + 1] - offsets[e] when no counts are given.
+// Segments need no alignment and may leave gaps; rows outside every segment are
+// neither used nor written.
+#pragma once
+
+#include "moe_common.cuh"
+
+namespace moe {
+
+constexpr int kMaxGroups = 256;   // experts of a grouped product (the tile table is in shared memory)
+
+struct Segments {
+    const int32_t* offsets;   // [E + 1] device
+    const int32_t* counts;    // [E] device or null
+    int E;
+    int M;                    // rows of the row buffers
+};
+
+// Tiles of `tile` rows: expert e owns tiles [base[e], base[e + 1]).
+struct SegTable {
+    int row0[kMaxGroups];
+    int rows[kMaxGroups];
+    int base[kMaxGroups + 1];
+    int total;
+};
+
+// Built by one whole warp.  A segment outside the row buffers, or one that runs
+// into the next, records MOE_ERR_DEVICE and leaves the table without tiles.
+__device__ __forceinline__ void build_segments(SegTable* t, const Segments& s, int tile, int* status) {
+    const int lane = threadIdx.x & 31;
+    int carry = 0;
+    bool ok = true;
+    for (int e0 = 0; e0 < s.E; e0 += 32) {
+        const int e = e0 + lane;
+        int tiles = 0;
+        if (e < s.E) {
+            const int o0 = s.offsets[e], o1 = s.offsets[e + 1];
+            const int n = s.counts ? s.counts[e] : o1 - o0;
+            const bool good = o0 >= 0 && o1 >= o0 && o1 <= s.M && n >= 0 && n <= o1 - o0;
+            ok = ok && good;
+            tiles = good ? (n + tile - 1) / tile : 0;
+            t->row0[e] = good ? o0 : 0;
+            t->rows[e] = good ? n : 0;
+        }
+        int inc = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += v;
+        }
+        if (e < s.E) t->base[e] = carry + inc - tiles;
+        carry += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (lane == 0) {
+        if (!ok) record_status(status, MOE_ERR_DEVICE);
+        t->base[s.E] = carry;
+        t->total = ok ? carry : 0;
+    }
+    if (!ok) {
+        __syncwarp();
+        for (int e = lane; e < s.E; e += 32) t->rows[e] = 0;
+    }
+}
+
+// The expert that owns a tile: the last e with base[e] <= tile (tile < base[E]).
+__device__ __forceinline__ int segment_of(const SegTable* t, int E, int tile) {
+    int lo = 0, hi = E;   // base[lo] <= tile < base[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t->base[mid] <= tile) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+enum GroupedOp : int {
+    kGroupedMm = 0,     // y_r  = W_e x_r
+    kGroupedDgrad = 1,  // dx_r = W_e^T dy_r
+    kGroupedWgrad = 2,  // dW_e = sum_r dy_r x_r^T
+};
+
+struct GroupedArgs {
+    GroupedOp op;
+    const void* rows;   // mm: x [M][K]; dgrad, wgrad: dy [M][N]
+    const void* other;  // mm, dgrad: W [E][N][K]; wgrad: x [M][K]
+    void* out;          // mm [M][N], dgrad [M][K], wgrad [E][N][K]
+    Segments seg;
+    int N, K;
+    bool in16, out16;   // bfloat16 instead of float
+    // adapters (mm only; A == null: none)
+    const void* A;      // [L][E][R][K]
+    const void* B;      // [L][E][N][R]
+    const float* scale; // [L]
+    const int32_t* adapter;   // [M], -1: none
+    int L, R;
+    uint8_t* ws;        // adapters: the shrunken rows u and the lists of the tiles
+    int num_sms;
+    int* status;
+    long long wait_ns;
+};
+
+cudaError_t launch_grouped_simt(const GroupedArgs& a, cudaStream_t s);
+cudaError_t launch_lora_shrink(const GroupedArgs& a, cudaStream_t s);
+size_t lora_workspace_bytes(int M, int E, int L, int R);
+
+}  // namespace moe

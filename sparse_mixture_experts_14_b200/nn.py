@@ -11,6 +11,10 @@ gates over the k, SwiGLU experts W2 (SiLU(W1 x) * W3 x), gate-weighted sum
 With alpha != 0 the gradient also holds the load-balance loss alpha E sum f p of
 the batch's routing (subsection "ロードバランス損失"); its value comes from
 moe_route_stats.
+
+GroupedLinear is the grouped product alone (moe_grouped_mm with both gradients), for
+experts of another form around moe_dispatch's segments; clip_grad_norm_ clips the
+.grad of a list of parameters by their global norm (moe_clip_grads).
 """
 from __future__ import annotations
 
@@ -18,8 +22,8 @@ import math
 
 import torch
 
-from . import (MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_PATH_TRAIN, moe_backward_ws, moe_forward, moe_forward_ws,
-               moe_train_workspace_size)
+from . import (MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_PATH_TRAIN, moe_backward_ws, moe_clip_grads, moe_forward,
+               moe_forward_ws, moe_grouped_dgrad, moe_grouped_mm, moe_grouped_wgrad, moe_train_workspace_size)
 
 
 class MoEFunction(torch.autograd.Function):
@@ -73,3 +77,51 @@ class SparseMoE(torch.nn.Module):
         else:
             out = moe_forward(x2, *(w.detach() for w in weights), self.k)
         return out.reshape(shape)
+
+
+class GroupedMmFunction(torch.autograd.Function):
+    """y_r = W_e x_r for the rows of every expert's segment, with gradients for x and W.
+
+    Rows in no segment are zero in y and in the gradient of x.
+    """
+
+    @staticmethod
+    def forward(ctx, x, W, offsets, counts=None):
+        y = torch.zeros((x.shape[0], W.shape[1]), dtype=x.dtype, device=x.device)
+        moe_grouped_mm(x, W, offsets, counts, out=y)
+        ctx.save_for_backward(x, W, offsets, counts)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, W, offsets, counts = ctx.saved_tensors
+        dy = dy.contiguous()
+        dx = dW = None
+        if ctx.needs_input_grad[0]:
+            dx = moe_grouped_dgrad(dy, W, offsets, counts, out=torch.zeros_like(x))
+        if ctx.needs_input_grad[1]:
+            dW = moe_grouped_wgrad(dy, x, offsets, counts)
+        return dx, dW, None, None
+
+
+class GroupedLinear(torch.nn.Module):
+    """One bias-free linear map per expert over ragged segments of rows: W [E][out][in]."""
+
+    def __init__(self, E: int, in_features: int, out_features: int, dtype=torch.bfloat16, device="cuda"):
+        super().__init__()
+        self.W = torch.nn.Parameter(torch.randn(E, out_features, in_features, dtype=dtype, device=device) /
+                                    math.sqrt(in_features))
+
+    def forward(self, x, offsets, counts=None):
+        return GroupedMmFunction.apply(x.contiguous(), self.W, offsets, counts)
+
+
+def clip_grad_norm_(parameters, max_norm: float, eps: float = 1e-6):
+    """Clip the gradients of the parameters (one, or an iterable) in place by their global 2-norm; returns
+    the norm before clipping (float32 [1], on the device).  No host synchronisation."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
+    grads = [p.grad for p in parameters if p.grad is not None]
+    if not grads:
+        return torch.zeros(1)
+    return moe_clip_grads(grads, max_norm, eps=eps)[0]

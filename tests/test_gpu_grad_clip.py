@@ -1,0 +1,178 @@
+"""The global gradient norm and clipping against their formulas in 64 bits: mixed types, lengths and
+alignments, many tensors, values at the ends of the range, in place and not, graphs, after a backward."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import sparse_mixture_experts_14_b200 as m
+    return m
+
+
+def _grads(spec, seed=0, scale=1e-2):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    dt = {"b": torch.bfloat16, "f": torch.float32}
+    return [(torch.randn(n, generator=gen, device="cuda") * scale).to(dt[t]) for t, n in spec]
+
+
+def _norm64(grads):
+    return math.sqrt(sum(g.double().pow(2).sum().item() for g in grads))
+
+
+def _check_norm(norm, grads):
+    want = _norm64(grads)
+    # fp32 sums of at most 32 squares (relative error 32 * 2^-24 at most, halved by the root), the result's
+    # rounding 2^-24, fp64 elsewhere
+    assert abs(norm.item() - want) <= (16 + 1) * 2.0 ** -24 * want * 1.01
+    return want
+
+
+def _check_scaled(outs, grads, max_norm, eps):
+    n = _norm64(grads)
+    c = min(1.0, max_norm / (n + eps))
+    for o, g in zip(outs, grads):
+        # the factor is off by the norm's fp32 sums (16 * 2^-24) and its own rounding (2^-24), the product by
+        # its fp32 rounding (2^-24) and by the output's
+        tol = 19 * 2.0 ** -24 + (torch.finfo(torch.bfloat16).eps / 2 if o.dtype == torch.bfloat16 else 0)
+        want = g.double() * c
+        assert ((o.double() - want).abs() <= tol * want.abs()).all()
+
+
+SPECS = {
+    "one": [("f", 1)],
+    "lengths": [("b", 1), ("f", 3), ("b", 8), ("f", 8192), ("b", 8193), ("f", 8191), ("b", 70001), ("f", 4)],
+    "empty-among": [("b", 0), ("f", 1000), ("b", 0), ("b", 77)],
+    "many": [("bf"[i % 2], 1 + (i * 37) % 300) for i in range(700)],
+    "large": [("b", 30_000_007), ("f", 9_000_001), ("b", 5)],
+}
+
+
+@pytest.mark.parametrize("spec", SPECS)
+@pytest.mark.parametrize("max_norm", [0.25, 1e9, float("inf"), 0.0])
+def test_clip(moe, spec, max_norm):
+    grads = _grads(SPECS[spec])
+    keep = [g.clone() for g in grads]
+    norm = moe.moe_grad_norm(grads)
+    _check_norm(norm, keep)
+    out = [torch.full_like(g, 5.0) for g in grads]
+    n2, outs = moe.moe_clip_grads(grads, max_norm, out=out)
+    assert torch.equal(n2, norm) and all(a is b for a, b in zip(outs, out))
+    assert all(torch.equal(g, k) for g, k in zip(grads, keep)), "the inputs were written"
+    _check_scaled(out, keep, max_norm, 1e-6)
+    n3, same = moe.moe_clip_grads(grads, max_norm)
+    assert torch.equal(n3, norm) and all(a is b for a, b in zip(same, grads))
+    assert all(torch.equal(g, o) for g, o in zip(grads, out)), "in place differs"
+
+
+def test_views_off_alignment(moe):
+    flat = torch.randn(100_000, device="cuda")
+    half = flat.to(torch.bfloat16)
+    grads = [flat[1:30_000], flat[30_001:30_004], half[3:9_000], half[9_001:50_000], flat[40_000:90_000]]
+    keep = [g.clone() for g in grads]
+    rest = flat[90_000:].clone()
+    norm, _ = moe.moe_clip_grads(grads, 1.0)
+    _check_norm(norm, keep)
+    _check_scaled(grads, keep, 1.0, 1e-6)
+    assert torch.equal(flat[90_000:], rest)
+
+
+@pytest.mark.parametrize("value", [1e-20, 1e-30, 1e18, 3e19, 1e38, 1e-40])
+def test_range(moe, value):
+    """Squares that fp32 cannot hold: the norm of n equal values is value sqrt(n)."""
+    n = 40_000
+    grads = [torch.full((n,), value, device="cuda"), torch.full((n,), value, device="cuda").to(torch.bfloat16)]
+    want = _norm64(grads)
+    got = moe.moe_grad_norm(grads).item()
+    if want > 3.4028234e38:
+        assert got == float("inf")
+    else:
+        # a result below the normal range is rounded to a multiple of 2^-149
+        assert abs(got - want) <= 18 * 2.0 ** -24 * want + 2.0 ** -149
+
+
+def test_mixed_magnitudes(moe):
+    """Small values beside large ones in one thread's group, none lost above the bound."""
+    g = torch.full((65536,), 1e-12, device="cuda")
+    g[::97] = 3e10
+    _check_norm(moe.moe_grad_norm([g]), [g])
+
+
+@pytest.mark.parametrize("where", [0, 12345, 65535])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_nan_and_inf(moe, where, dtype):
+    g = [torch.ones(65536, device="cuda", dtype=dtype), torch.ones(100, device="cuda")]
+    g[0][where] = float("nan")
+    norm, out = moe.moe_clip_grads(g, 1.0, out=[torch.zeros_like(t) for t in g])
+    assert norm.isnan().all() and all(o.isnan().all() for o in out)
+    g[0][where] = -float("inf")
+    norm, out = moe.moe_clip_grads(g, 1.0, out=[torch.zeros_like(t) for t in g])
+    assert norm.item() == float("inf")
+    assert out[0][where].isnan() and int(out[0].isnan().sum()) == 1 and (out[1] == 0).all()
+
+
+def test_zero_gradients_and_empty_list(moe):
+    g = [torch.zeros(5000, device="cuda"), torch.zeros(0, device="cuda", dtype=torch.bfloat16)]
+    norm, out = moe.moe_clip_grads(g, 1.0, eps=0.0)
+    assert norm.item() == 0.0 and (out[0] == 0).all()
+    norm = torch.full((1,), 3.0, device="cuda")
+    assert moe.moe_grad_norm([], norm=norm).item() == 0.0
+    norm.fill_(3.0)
+    assert moe.moe_clip_grads([], 1.0, norm=norm)[0].item() == 0.0
+
+
+def test_overlapping_outputs_are_refused(moe):
+    buf = torch.ones(1000, device="cuda")
+    a, b = buf[:600], buf[500:]
+    for args in (([a, b], None), ([a, a], None), ([a.clone(), b.clone()], [a, b]),
+                 ([a, b.clone()], [b[:100].clone().resize_(600), a[:500]]), ([buf[1:]], [buf[:-1]])):
+        with pytest.raises(moe.MoEError):
+            moe.moe_clip_grads(args[0], 1.0, out=args[1])
+    assert (buf == 1).all()
+    moe.moe_grad_norm([a, b, a])   # reading twice is fine
+
+
+def test_repeatable_on_another_stream_and_in_a_graph(moe):
+    grads = _grads(SPECS["lengths"] + [("b", 3_000_000)], seed=4)
+    out = [torch.empty_like(g) for g in grads]
+    norm, _ = moe.moe_clip_grads(grads, 0.5, out=out)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        out2 = [torch.empty_like(g) for g in grads]
+        norm2, _ = moe.moe_clip_grads(grads, 0.5, out=out2)
+    side.synchronize()
+    assert torch.equal(norm, norm2) and all(torch.equal(a, b) for a, b in zip(out, out2))
+    g = torch.cuda.CUDAGraph()
+    nrm = torch.zeros(1, device="cuda")
+    with torch.cuda.graph(g):
+        moe.moe_clip_grads(grads, 0.5, out=out, norm=nrm)
+    for t in grads:
+        t.mul_(2)
+    g.replay()
+    torch.cuda.synchronize()
+    _check_norm(nrm, grads)
+    _check_scaled(out, grads, 0.5, 1e-6)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_after_the_layers_backward(moe, dtype):
+    """A training step: forward, backward, clip the dict of gradients."""
+    import moe_inputs
+    from moe_testlib import to_dev, upload
+    T, d, F, E, k = 150, 128, 256, 8, 2
+    args = upload(moe_inputs.make_inputs(T, d, F, E, k, dtype, seed=41))
+    code = moe.MOE_DTYPE_BF16 if dtype == "bf16" else moe.MOE_DTYPE_F32
+    ws = torch.empty(moe.moe_train_workspace_size(T, d, F, E, k, code), dtype=torch.uint8, device="cuda")
+    moe.moe_forward_ws(*args, k, path=moe.MOE_PATH_TRAIN, workspace=ws)
+    g, _ = moe.moe_backward_ws(*args, to_dev(moe_inputs.make_dout(T, d, dtype, seed=41), dtype), k, ws)
+    dx = g.pop("dx").clone()
+    keep = [t.clone() for t in g.values()]
+    norm, clipped = moe.moe_clip_grads(g, 0.1)
+    _check_norm(norm, keep)
+    _check_scaled(list(g.values()), keep, 0.1, 1e-6)
+    assert torch.isfinite(dx).all() and moe.moe_get_device_status() == moe.MOE_OK

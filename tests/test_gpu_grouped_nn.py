@@ -1,0 +1,98 @@
+"""GroupedLinear and clip_grad_norm_: autograd over the grouped products, with the layer's dispatch, and a
+training step captured into a graph while an eager graph of the same parameters lives."""
+import pytest
+import torch
+
+from grouped_testlib import DT, check, mm
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mods():
+    import sparse_mixture_experts_14_b200 as m
+    import sparse_mixture_experts_14_b200.nn as nn
+    return m, nn
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients(mods, dtype):
+    moe, nn = mods
+    counts = [70, 0, 3]
+    off = torch.tensor([0, 128, 128, 140], dtype=torch.int32, device="cuda")
+    cnt = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    torch.manual_seed(3)
+    lin = nn.GroupedLinear(3, 72, 40, dtype=DT[dtype])
+    x = torch.randn(140, 72, device="cuda").to(DT[dtype]).requires_grad_()
+    dy = torch.randn(140, 40, device="cuda").to(DT[dtype])
+    y = lin(x, off, cnt)
+    y.backward(dy)
+    gap = [r for r in range(140) if not (r < 70 or 128 <= r < 131)]
+    assert (y[gap] == 0).all() and (x.grad[gap] == 0).all()
+    for e, (s, n) in enumerate(zip([0, 128, 128], counts)):
+        r = slice(s, s + n)
+        W = lin.W.detach()[e]
+        check(y.detach()[r], *mm(x.detach()[r], W.t()), 72, "y")
+        check(x.grad[r], *mm(dy[r], W), 40, "dx")
+        check(lin.W.grad[e], *mm(dy[r].t(), x.detach()[r]), n, "dW")
+    assert moe.moe_get_device_status() == moe.MOE_OK
+
+
+def test_only_the_asked_gradients(mods):
+    moe, nn = mods
+    off = torch.tensor([0, 5, 9], dtype=torch.int32, device="cuda")
+    lin = nn.GroupedLinear(2, 64, 64)
+    x = torch.randn(9, 64, device="cuda", dtype=torch.bfloat16)
+    lin(x, off).float().sum().backward()
+    assert lin.W.grad is not None
+    lin.W.requires_grad_(False)
+    lin.W.grad = None
+    x.requires_grad_()
+    lin(x, off).float().sum().backward()
+    assert x.grad is not None and lin.W.grad is None
+
+
+def test_training_step_in_a_graph(mods):
+    """Two grouped layers, their gradients and the clip, captured; an eager step before gives the same."""
+    moe, nn = mods
+    torch.manual_seed(5)
+    off = torch.tensor([0, 40, 47, 47, 200], dtype=torch.int32, device="cuda")
+    a, b = nn.GroupedLinear(4, 128, 256), nn.GroupedLinear(4, 256, 128)
+    params = [a.W, b.W]
+    x = torch.randn(200, 128, device="cuda", dtype=torch.bfloat16)
+
+    def step():
+        y = b(torch.relu(a(x, off)), off)
+        grads = torch.autograd.grad(y.float().pow(2).sum(), params)
+        return moe.moe_clip_grads(list(grads), 1.0)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            norm, eager = step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gnorm, captured = step()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(norm, gnorm) and all(torch.equal(p, q) for p, q in zip(eager, captured))
+    total = sum(t.double().pow(2).sum().item() for t in captured) ** 0.5
+    assert abs(total - 1.0) <= 2.0 ** -8   # every clipped gradient rounded to bf16
+    assert moe.moe_get_device_status() == moe.MOE_OK
+
+
+def test_clip_grad_norm_on_the_layer(mods):
+    moe, nn = mods
+    torch.manual_seed(6)
+    layer = nn.SparseMoE(d=128, ffn=256, E=8, k=2)
+    layer(torch.randn(64, 128, device="cuda", dtype=torch.bfloat16)).float().pow(2).sum().backward()
+    keep = [p.grad.clone() for p in layer.parameters()]
+    want = sum(t.double().pow(2).sum().item() for t in keep) ** 0.5
+    norm = nn.clip_grad_norm_(layer.parameters(), want / 4)
+    assert abs(norm.item() - want) <= 18 * 2.0 ** -24 * want
+    for p, k in zip(layer.parameters(), keep):
+        w = k.double() * (want / 4 / (want + 1e-6))
+        assert ((p.grad.double() - w).abs() <= (2.0 ** -8 + 2.0 ** -18) * w.abs()).all()
+    assert nn.clip_grad_norm_([torch.nn.Parameter(torch.ones(3, device="cuda"))], 1.0).item() == 0.0
