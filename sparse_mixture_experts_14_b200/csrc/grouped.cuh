@@ -105,6 +105,7 @@ struct GroupedArgs {
 };
 
 cudaError_t launch_grouped_simt(const GroupedArgs& a, cudaStream_t s);
+cudaError_t launch_grouped_tc(const GroupedArgs& a, cudaStream_t s);   // bf16 operands, M > 0
 cudaError_t launch_lora_shrink(const GroupedArgs& a, cudaStream_t s);
 size_t lora_workspace_bytes(int M, int E, int L, int R);
 

@@ -58,7 +58,12 @@ moe_status run(GroupedOp op, const void* rows, const void* other, const int32_t*
     if (st != MOE_OK || (M == 0 && op != kGroupedWgrad)) return st;
     const DeviceScope scope(out, false);
     if (!on_device(&a, scope.device())) return MOE_ERR_CUDA;
-    return launch_grouped_simt(a, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    cudaError_t e;
+    if (M == 0)   // no rows: every weight gradient is zero
+        e = cudaMemsetAsync(out, 0, (size_t)E * N * K * (a.out16 ? 2 : 4), s);
+    else
+        e = a.in16 ? launch_grouped_tc(a, s) : launch_grouped_simt(a, s);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
