@@ -22,8 +22,15 @@
 // A pair of CTAs computes a 256 x (up to 256) tile with tcgen05.mma.cta_group::2,
 // each CTA holding 128 features and half of the columns' operand.  Persistent, one
 // CTA per SM: warp 0 TMA producer into a ring of 64-deep stages, warp 1 MMA issuer
-// (in the pair's leader), warps 2-5 epilogue of the CTA's 128 features out of two
-// alternating accumulators, further warps for the ends of wgrad's segments.
+// (in the pair's leader), 4 or 8 epilogue warps for the CTA's 128 features out of two
+// alternating accumulators, a further warp for the ends of wgrad's segments.
+//
+// fp32 outputs: the tensor cores truncate when they add to the accumulator, which
+// costs 1.8e-8 of the result per 16-deep step, all in one direction (1.6e-5 at a
+// reduction of 14336, where a blocked fp32 sum has 3e-7).  So the accumulator takes
+// 512 of the reduction at a time, and the epilogue adds these partial sums in
+// registers with rounding, while the MMAs go on in the other accumulator.  bf16
+// outputs, whose own rounding is 2^-9, take the whole reduction in one.
 //
 // wgrad: the last 64-row block of a segment also holds rows of the next one, which
 // must not count, whatever they hold (NaN times zero is NaN).  The MMA stops at the
@@ -50,6 +57,7 @@ constexpr int BOX = 64;                    // MN-major operands: 64-wide boxes
 constexpr uint32_t MN_LBO = BOX * BK * 2;
 constexpr uint32_t MN_SBO = 1024;
 constexpr int TMEM_COLS = 2 * BN;
+constexpr int CHUNK = 512 / BK;            // blocks per accumulator, fp32 outputs
 
 struct Maps {
     CUtensorMap a;
@@ -86,7 +94,8 @@ struct Cfg {
     static constexpr bool A_MN = OP != kGroupedMm;
     static constexpr bool B_MN = WGRAD;
     static constexpr int AUX_WARPS = WGRAD ? 1 : 0;
-    static constexpr int THREADS = 32 * (6 + AUX_WARPS);
+    static constexpr int EPI_WARPS = OUT16 ? 4 : 8;
+    static constexpr int THREADS = 32 * (2 + EPI_WARPS + AUX_WARPS);
     static constexpr int SMEM = NST * STAGE + (int)sizeof(Ctrl) + 1024;
 };
 
@@ -166,7 +175,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&ctrl->tfull[b], 1);
-            ptx::mbar_init(&ctrl->tempty[b], 2 * 4);
+            ptx::mbar_init(&ctrl->tempty[b], 2 * CF::EPI_WARPS);
         }
         ptx::mbar_init(&ctrl->drain, 1);
         ctrl->abort = 0;
@@ -280,14 +289,16 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
             for (int tile = cluster; tile < total && !aborted; tile += nclusters) {
                 const Tile t = decode<WGRAD>(ctrl, p, tile);
                 const uint32_t idesc = ptx::idesc_bf16_f32(2 * BM, t.nn, CF::A_MN, CF::B_MN);
-                if (!ptx::mbar_wait(&ctrl->tempty[acc], acc_phase ^ 1u, wc)) {
-                    aborted = true;
-                    break;
-                }
-                ptx::tc_fence_after_sync();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+                uint32_t d_tmem = 0;
                 for (int kb = 0; kb < t.nkb; ++kb) {
-                    bool ok = ptx::mbar_wait(&ctrl->full[stage], phase, wc);
+                    const bool first = OUT16 ? kb == 0 : kb % CHUNK == 0;   // of an accumulator
+                    bool ok = true;
+                    if (first) {
+                        ok = ptx::mbar_wait(&ctrl->tempty[acc], acc_phase ^ 1u, wc);
+                        ptx::tc_fence_after_sync();
+                        d_tmem = tmem_base + (uint32_t)(acc * BN);
+                    }
+                    ok = ok && ptx::mbar_wait(&ctrl->full[stage], phase, wc);
                     int slices = BK / 16;
                     if (WGRAD && kb == t.nkb - 1) {
                         slices = (t.rows - kb * BK + 15) / 16;
@@ -310,7 +321,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
                                                      : ptx::desc_kmajor_sw128(a0 + kk * 32);
                         const uint64_t db = CF::B_MN ? ptx::desc_mnmajor_sw128(b0 + kk * 2048, MN_LBO, MN_SBO)
                                                      : ptx::desc_kmajor_sw128(b0 + kk * 32);
-                        ptx::tc_mma_bf16_pair(d_tmem, da, db, idesc, (kb | kk) != 0);
+                        ptx::tc_mma_bf16_pair(d_tmem, da, db, idesc, !(first && kk == 0));
                     }
                     ptx::tc_commit_pair_multicast(&ctrl->empty[stage], 0x3);
                     issued = true;
@@ -318,42 +329,44 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
                         stage = 0;
                         phase ^= 1u;
                     }
+                    if (kb == t.nkb - 1 || (!OUT16 && kb % CHUNK == CHUNK - 1)) {
+                        ptx::tc_commit_pair_multicast(&ctrl->tfull[acc], 0x3);
+                        acc ^= 1;
+                        if (acc == 0) acc_phase ^= 1u;
+                    }
                 }
-                if (aborted) break;
-                ptx::tc_commit_pair_multicast(&ctrl->tfull[acc], 0x3);
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1u;
             }
             if ((aborted || ctrl->abort) && issued) {
                 ptx::tc_commit_pair(&ctrl->drain);
                 ptx::mbar_wait_drain(&ctrl->drain, 0, 100000000ull);
             }
         }
-    } else if (warp < 6) {
+    } else if (warp < 2 + CF::EPI_WARPS) {
         // ---------------------------------------------------------------- epilogue (both CTAs)
         const int q = warp & 3;   // TMEM lane quarter this warp may access
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int tile = cluster; tile < total; tile += nclusters) {
+        bool ok = true;
+        for (int tile = cluster; tile < total && ok; tile += nclusters) {
             const Tile t = decode<WGRAD>(ctrl, p, tile);
-            bool ok = ptx::mbar_wait(&ctrl->tfull[acc], acc_phase, wc);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            ptx::tc_fence_after_sync();
-            const uint32_t taddr = tmem_base + (uint32_t)(acc * BN) + ((uint32_t)(q * 32) << 16);
             const int f = t.f0 + (int)rank * BM + q * 32 + lane;
-            const bool none = t.nkb == 0;   // no rows: the accumulator was never written, the sum is zero
             const size_t row0 = WGRAD ? (size_t)t.e * p.C + t.c0 : (size_t)t.c0;
+            if (OUT16) {
+                // (no rows in the segment: nothing was accumulated, the sum is zero)
+                if (t.nkb > 0) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->tfull[acc], acc_phase, wc));
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                const uint32_t taddr = tmem_base + (uint32_t)(acc * BN) + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
-            for (int c = 0; c < t.nn; c += 32) {
-                uint32_t r[32];
-                ptx::tmem_ld_32x32b_x32(taddr + c, r);
-                ptx::tmem_ld_wait();
-                if (none) {
+                for (int c = 0; c < t.nn; c += 32) {
+                    uint32_t r[32];
+                    if (t.nkb > 0) {
+                        ptx::tmem_ld_32x32b_x32(taddr + c, r);
+                        ptx::tmem_ld_wait();
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = 0u;
-                }
-                if (OUT16) {
+                        for (int i = 0; i < 32; ++i) r[i] = 0u;
+                    }
                     // neighbouring lanes swap one of two columns: the even lane stores features f, f + 1 of
                     // column i, the odd one features f - 1, f of column i + 1 (F is a multiple of 8)
                     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (f & ~1);
@@ -367,19 +380,49 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
                         if (col < t.valid && f < p.F)
                             *reinterpret_cast<uint32_t*>(out + (row0 + col) * (size_t)p.F) = v;
                     }
-                } else {
-                    float* out = static_cast<float*>(p.out) + f;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (c + i < t.valid && f < p.F) out[(row0 + c + i) * (size_t)p.F] = __uint_as_float(r[i]);
                 }
+                if (t.nkb == 0) continue;
+                // the accumulator is free once every lane's tcgen05.ld has completed
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive_cluster_relaxed(ptx::map_to_rank(ptx::smem_addr(&ctrl->tempty[acc]), 0));
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            } else {
+                // two warps per lane quarter, each with half of the columns (a multiple of 16)
+                const int half = t.nn / 2, c0 = (warp - 2) / 4 * half;
+                float sum[BN / 2];
+#pragma unroll
+                for (int i = 0; i < BN / 2; ++i) sum[i] = 0.f;
+                for (int kb = 0; kb < t.nkb && ok; kb += CHUNK) {
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->tfull[acc], acc_phase, wc));
+                    if (!ok) break;
+                    ptx::tc_fence_after_sync();
+                    const uint32_t taddr = tmem_base + (uint32_t)(acc * BN + c0) + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+                    for (int c = 0; c < BN / 2; c += 16) {
+                        if (c < half) {
+                            uint32_t r[16];
+                            ptx::tmem_ld_32x32b_x16(taddr + c, r);
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(r[i]);
+                        }
+                    }
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        ptx::mbar_arrive_cluster_relaxed(ptx::map_to_rank(ptx::smem_addr(&ctrl->tempty[acc]), 0));
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
+                }
+                if (!ok) break;
+                float* out = static_cast<float*>(p.out) + (row0 + c0) * (size_t)p.F + f;
+#pragma unroll
+                for (int i = 0; i < BN / 2; ++i)
+                    if (i < half && c0 + i < t.valid && f < p.F) out[i * (size_t)p.F] = sum[i];
             }
-            // the accumulator is free once every lane's tcgen05.ld has completed
-            ptx::tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::map_to_rank(ptx::smem_addr(&ctrl->tempty[acc]), 0));
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1u;
         }
     } else if (WGRAD) {
         // ---------------------------------------------------------------- ends of segments (both CTAs)
