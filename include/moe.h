@@ -565,7 +565,9 @@ MOE_API moe_status moe_grouped_wgrad(const void* dy, const void* x, const int32_
  *   (device): the row's adapter in [0, L), or -1 for none.  Rows of one adapter
  *   need not be neighbours.  E = 1 with offsets {0, M}: one shared projection.
  * s_a A x is rounded once to bf16 (the second product's operand type); the sum
- * of both products is rounded once.  An id outside [-1, L) in a segment records
+ * of both products is rounded once.  A NaN or Inf in an adapter reaches the
+ * rows of that adapter only (other rows may be summed in another order then).
+ * An id outside [-1, L) in a segment records
  * MOE_ERR_DEVICE.  Sizes: as moe_grouped_mm; R a multiple of 8, at most
  * MOE_LORA_MAX_RANK.  workspace: moe_grouped_lora_workspace_size() bytes
  * (device, 256-byte aligned, not in use by another call in flight).

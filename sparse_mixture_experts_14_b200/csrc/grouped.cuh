@@ -104,9 +104,45 @@ struct GroupedArgs {
     long long wait_ns;
 };
 
-cudaError_t launch_grouped_simt(const GroupedArgs& a, cudaStream_t s);
-cudaError_t launch_grouped_tc(const GroupedArgs& a, cudaStream_t s);   // bf16 operands, M > 0
-cudaError_t launch_lora_shrink(const GroupedArgs& a, cudaStream_t s);
-size_t lora_workspace_bytes(int M, int E, int L, int R);
+// Rows of a column tile of a segment of n rows: n is cut into ceil(n / 256) tiles of equal height, a
+// multiple of 32.
+constexpr int kColumnTile = 256;
+__host__ __device__ inline int column_tile_height(int n) {
+    const int tt = (n + kColumnTile - 1) / kColumnTile;
+    return tt > 0 ? ((n + tt - 1) / tt + 31) / 32 * 32 : 32;
+}
+
+// The adapters as the products' kernels see them.  u is a workspace buffer [M][R16], R16 = R rounded
+// up to 16 (zeros behind R); rows without an adapter hold nothing.
+struct LoraView {
+    const __nv_bfloat16* B;        // [L][E][N][R]
+    const int32_t* adapter;        // [M]
+    __nv_bfloat16* u;              // [M][R16]
+    int32_t* tile_list;            // [column tiles][256]: the adapters that occur in the tile, each once
+    int32_t* tile_count;           // [column tiles]
+    int L, R, R16;
+};
+
+inline size_t lora_tiles(int M, int E) { return (size_t)M / kColumnTile + E; }
+inline size_t lora_u_bytes(int M, int R) { return align_up((size_t)M * ((R + 15) / 16 * 16) * 2, 256); }
+inline size_t lora_workspace_bytes(int M, int E, int R) {
+    return lora_u_bytes(M, R) + align_up(lora_tiles(M, E) * (kColumnTile + 1) * 4, 256);
+}
+inline LoraView lora_view(const GroupedArgs& a) {
+    LoraView v;
+    v.B = static_cast<const __nv_bfloat16*>(a.B);
+    v.adapter = a.adapter;
+    v.u = reinterpret_cast<__nv_bfloat16*>(a.ws);
+    v.tile_list = reinterpret_cast<int32_t*>(a.ws + lora_u_bytes(a.seg.M, a.R));
+    v.tile_count = v.tile_list + lora_tiles(a.seg.M, a.seg.E) * kColumnTile;
+    v.L = a.L;
+    v.R = a.R;
+    v.R16 = (a.R + 15) / 16 * 16;
+    return v;
+}
+
+cudaError_t launch_grouped_simt(const GroupedArgs& a, cudaStream_t s);   // float
+cudaError_t launch_grouped_tc(const GroupedArgs& a, cudaStream_t s);     // bfloat16, M > 0
+cudaError_t launch_lora_shrink(const GroupedArgs& a, cudaStream_t s);    // u and the tiles' lists
 
 }  // namespace moe

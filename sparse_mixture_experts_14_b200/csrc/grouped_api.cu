@@ -90,7 +90,7 @@ moe_status moe_grouped_wgrad(const void* dy, const void* x, const int32_t* offse
 
 size_t moe_grouped_lora_workspace_size(int M, int E, int L, int R) {
     if (M < 0 || E <= 0 || L <= 0 || R <= 0 || E > kMaxGroups || R > MOE_LORA_MAX_RANK || R % 8 != 0) return 0;
-    return lora_workspace_bytes(M, E, L, R);
+    return lora_workspace_bytes(M, E, R);
 }
 
 moe_status moe_grouped_lora(const void* x, const void* W, const int32_t* offsets, const int32_t* counts, const void* A,
@@ -121,13 +121,13 @@ moe_status moe_grouped_lora(const void* x, const void* W, const int32_t* offsets
     if (!A || !B || !scale || !adapter || !aligned(A, 16) || !aligned(B, 16) || !aligned(scale, 4) ||
         !aligned(adapter, 4))
         return MOE_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < lora_workspace_bytes(M, E, L, R))
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < lora_workspace_bytes(M, E, R))
         return MOE_ERR_WORKSPACE;
     a.ws = static_cast<uint8_t*>(workspace);
     const DeviceScope scope(y, false);
     if (!on_device(&a, scope.device())) return MOE_ERR_CUDA;
     if (launch_lora_shrink(a, stream) != cudaSuccess) return MOE_ERR_CUDA;
-    return launch_grouped_simt(a, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return launch_grouped_tc(a, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

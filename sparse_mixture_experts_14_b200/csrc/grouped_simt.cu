@@ -65,8 +65,7 @@ struct Operand {
 template <typename TI, typename TO, int OP>
 __global__ void __launch_bounds__(256) grouped_simt_kernel(const TI* __restrict__ rows, const TI* __restrict__ other,
                                                            TO* __restrict__ out, const Segments seg, int N, int K,
-                                                           const TI* __restrict__ Bl, const float* __restrict__ u,
-                                                           const int32_t* __restrict__ adapter, int L, int R, int* status) {
+                                                           int* status) {
     pdl_trigger();
     pdl_wait();
     __shared__ SegTable tab;
@@ -156,21 +155,6 @@ __global__ void __launch_bounds__(256) grouped_simt_kernel(const TI* __restrict_
     for (int i = 0; i < 8; ++i) {
         const int m = (i >> 2) * 64 + ty * 4 + (i & 3);
         if (m >= m_rows) continue;
-        if (OP == kGroupedMm && u) {
-            const int id = adapter[row0 + m];
-            if (id >= 0 && id < L) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int n = (j >> 2) * 64 + tx * 4 + (j & 3);
-                    if (n >= n_cols) continue;
-                    const TI* bl = Bl + (((size_t)id * seg.E + e) * N + col0 + n) * R;
-                    for (int q = 0; q < R; q += 4) {
-                        const float4 v = load4(bl + q), w = load4(u + (size_t)(row0 + m) * R + q);
-                        acc[i][j] += v.x * w.x + v.y * w.y + v.z * w.z + v.w * w.w;
-                    }
-                }
-            }
-        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int n = h * 64 + tx * 4;
@@ -193,8 +177,7 @@ cudaError_t launch(const GroupedArgs& a, cudaStream_t s) {
     if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
     return launch_pdl(grouped_simt_kernel<TI, TO, OP>, dim3((unsigned)tiles), dim3(256), 0, s,
                       static_cast<const TI*>(a.rows), static_cast<const TI*>(a.other), static_cast<TO*>(a.out), a.seg,
-                      a.N, a.K, static_cast<const TI*>(a.B), a.A ? reinterpret_cast<const float*>(a.ws) : nullptr,
-                      a.adapter, a.L, a.R, a.status);
+                      a.N, a.K, a.status);
 }
 
 template <typename TI, typename TO>

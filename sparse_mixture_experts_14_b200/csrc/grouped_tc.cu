@@ -22,7 +22,7 @@
 // A pair of CTAs computes a 256 x (up to 256) tile with tcgen05.mma.cta_group::2,
 // each CTA holding 128 features and half of the columns' operand.  Persistent, one
 // CTA per SM: warp 0 TMA producer into a ring of 64-deep stages, warp 1 MMA issuer
-// (in the pair's leader), 4 or 8 epilogue warps for the CTA's 128 features out of two
+// (in the pair's leader), 8 or 16 epilogue warps for the CTA's 128 features out of two
 // alternating accumulators, a further warp for the ends of wgrad's segments.
 //
 // fp32 outputs: the tensor cores truncate when they add to the accumulator, which
@@ -31,6 +31,14 @@
 // 512 of the reduction at a time, and the epilogue adds these partial sums in
 // registers with rounding, while the MMAs go on in the other accumulator.  bf16
 // outputs, whose own rounding is 2^-9, take the whole reduction in one.
+//
+// Adapters (lora.cu computes u_r = s_a A_{a,e} x_r, bf16): B_{a,e} u_r is more of the
+// same reduction.  For every adapter that occurs among a tile's rows, in slices of 16
+// of its rank, the ring takes 128 x 16 boxes of B_{a,e} (A side, 32-byte swizzle) and,
+// written by two extra warps, the tile's rows of u with zeros in the rows of other
+// adapters (B side): one K = 16 MMA a slice, four slices a stage.  A zero does not
+// hide an infinity or NaN in another request's adapter, so where the sum is not finite
+// the epilogue computes that output again from its own terms alone.
 //
 // wgrad: the last 64-row block of a segment also holds rows of the next one, which
 // must not count, whatever they hold (NaN times zero is NaN).  The MMA stops at the
@@ -46,22 +54,25 @@
 namespace moe {
 namespace {
 
-constexpr int BM = 128;                    // features per CTA (256 per pair)
+constexpr int BM = 128;                    // features of one MMA per CTA (256 per pair)
 constexpr int BN = 256;                    // columns of a tile at most
 constexpr int BK = 64;                     // reduction per stage
-constexpr int NST = 6;
 constexpr int A_BYTES = BM * BK * 2;       // 16 KiB
 constexpr int B_BYTES = BN / 2 * BK * 2;   // 16 KiB
-constexpr int STAGE = A_BYTES + B_BYTES;
 constexpr int BOX = 64;                    // MN-major operands: 64-wide boxes
 constexpr uint32_t MN_LBO = BOX * BK * 2;
 constexpr uint32_t MN_SBO = 1024;
 constexpr int TMEM_COLS = 2 * BN;
 constexpr int CHUNK = 512 / BK;            // blocks per accumulator, fp32 outputs
 
+constexpr int SLICE = 16;                   // rank slice of one adapter MMA
+constexpr int SLICES = 4;                   // of a stage
+constexpr int SLICE_BYTES = BM * SLICE * 2; // 4 KiB, either side
+
 struct Maps {
     CUtensorMap a;
     CUtensorMap b[4];   // boxes of 16, 32, 64 and 128 rows (mm, dgrad); wgrad: b[0] only
+    CUtensorMap l;      // adapters: B_{a,e}, boxes of 16 x 128 features
 };
 
 struct Params {
@@ -69,16 +80,23 @@ struct Params {
     int F;            // features: the output's contiguous dimension
     int C;            // wgrad: columns (N)
     int red;          // mm, dgrad: length of the reduction
+    int f_fast;       // wgrad: feature blocks fastest, else column blocks
     void* out;
     int* status;
     long long wait_ns;
+    // adapters
+    LoraView lora;
+    const __nv_bfloat16* x;
+    const __nv_bfloat16* W;
 };
 
+constexpr int MAX_STAGES = 6;
+
 struct Ctrl {
-    uint64_t full[NST];     // leader: both CTAs' bytes of a stage landed
-    uint64_t empty[NST];    // each CTA: the MMAs that read a stage are done
-    uint64_t land[NST];     // wgrad: this CTA's bytes of a segment's last block landed
-    uint64_t ready[NST];    // leader: both CTAs prepared the stage by hand
+    uint64_t full[MAX_STAGES];     // leader: both CTAs' bytes of a stage landed
+    uint64_t empty[MAX_STAGES];    // each CTA: the MMAs that read a stage are done
+    uint64_t land[MAX_STAGES];     // wgrad: this CTA's bytes of a segment's last block landed
+    uint64_t ready[MAX_STAGES];    // leader: both CTAs prepared the stage by hand
     uint64_t tfull[2];      // each CTA: accumulator b holds a finished tile
     uint64_t tempty[2];     // leader: both CTAs' epilogues released accumulator b
     uint64_t drain;
@@ -88,45 +106,45 @@ struct Ctrl {
     SegTable seg;
 };
 
-template <int OP, bool OUT16>
+template <int OP, bool OUT16, int W, bool LORA>
 struct Cfg {
     static constexpr bool WGRAD = OP == kGroupedWgrad;
     static constexpr bool A_MN = OP != kGroupedMm;
     static constexpr bool B_MN = WGRAD;
-    static constexpr int AUX_WARPS = WGRAD ? 1 : 0;
-    static constexpr int EPI_WARPS = OUT16 ? 4 : 8;
+    static constexpr int AUX_WARPS = WGRAD ? 1 : LORA ? 2 : 0;
+    static constexpr int EPI_WARPS = OUT16 && W == 1 ? 8 : 16;
+    static constexpr int COLS = OUT16 ? 128 : 64;   // columns of an epilogue warp
     static constexpr int THREADS = 32 * (2 + EPI_WARPS + AUX_WARPS);
+    static constexpr int NST = W == 1 ? 6 : 4;
+    static constexpr int STAGE = W * A_BYTES + B_BYTES;
+    static constexpr int PAIR_F = W * 2 * BM;   // features of a pair's tile
+    static constexpr int ACCS = W == 1 ? 2 : 1; // accumulators in the 512 columns
     static constexpr int SMEM = NST * STAGE + (int)sizeof(Ctrl) + 1024;
 };
 
 // One tile: expert, first feature of the pair, first column (row of the row buffers, or n of dW),
 // columns of the MMA and those that count, 64-deep blocks.
 struct Tile {
-    int e, f0, c0, nn, valid, nkb, rows, row0;
+    int e, f0, c0, nn, valid, nkb, rows, row0, col_tile;
 };
 
-__host__ __device__ inline int tile_height(int n) {   // rows of a token tile of a segment of n rows
-    const int tt = (n + BN - 1) / BN;
-    return tt > 0 ? ((n + tt - 1) / tt + 31) / 32 * 32 : 32;
-}
-
-template <bool WGRAD>
+template <bool WGRAD, int PAIR_F>
 __device__ __forceinline__ Tile decode(const Ctrl* c, const Params& p, int tile) {
     Tile t;
-    const int nf = (p.F + 2 * BM - 1) / (2 * BM);
+    const int nf = (p.F + PAIR_F - 1) / PAIR_F;
     if (WGRAD) {
-        // columns fastest: the pairs at work share blocks of x
         const int nc = (p.C + BN - 1) / BN;
         t.e = tile / (nf * nc);
         const int local = tile - t.e * nf * nc;
-        const int fi = local / nc;
-        t.f0 = fi * 2 * BM;
-        t.c0 = (local - fi * nc) * BN;
+        const int fi = p.f_fast ? local % nf : local / nc;
+        t.f0 = fi * PAIR_F;
+        t.c0 = (p.f_fast ? local / nf : local % nc) * BN;
         t.rows = c->seg.rows[t.e];
         t.row0 = c->seg.row0[t.e];
         t.valid = min(BN, p.C - t.c0);
         t.nn = (t.valid + 31) / 32 * 32;
         t.nkb = (t.rows + BK - 1) / BK;
+        t.col_tile = 0;
     } else {
         // token tiles fastest: the pairs at work share blocks of the weights
         const int tok = tile / nf;   // any tile of the expert's group
@@ -135,14 +153,15 @@ __device__ __forceinline__ Tile decode(const Ctrl* c, const Params& p, int tile)
         const int local = tile - c->seg.base[t.e] * nf;
         const int fi = local / tt;
         t.rows = c->seg.rows[t.e];
-        const int h = tile_height(t.rows);
+        const int h = column_tile_height(t.rows);
         const int r = (local - fi * tt) * h;
-        t.f0 = fi * 2 * BM;
+        t.f0 = fi * PAIR_F;
         t.row0 = c->seg.row0[t.e];
         t.c0 = t.row0 + r;
         t.valid = min(h, t.rows - r);
         t.nn = h;
         t.nkb = (p.red + BK - 1) / BK;
+        t.col_tile = c->seg.base[t.e] + (local - fi * tt);
     }
     return t;
 }
@@ -150,11 +169,38 @@ __device__ __forceinline__ Tile decode(const Ctrl* c, const Params& p, int tile)
 // Index of the row box that holds n rows (n a multiple of 16, at most 128).
 __device__ __forceinline__ int box_of(int n) { return n <= 16 ? 0 : n <= 32 ? 1 : n <= 64 ? 2 : 3; }
 
-template <int OP, bool OUT16>
-__global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
+// Adapter slices of a tile: (adapters among its rows) x (slices of the rank).
+__device__ __forceinline__ int tile_slices(const LoraView& l, int col_tile) {
+    return l.tile_count[col_tile] * (l.R16 / SLICE);
+}
+
+// One output from its own terms: x_r W_e^T[f] and, with an adapter, u_r B_{a,e}^T[f].
+__device__ __noinline__ float recompute(const Params& p, int e, size_t r, int f) {
+    const __nv_bfloat16* w = p.W + ((size_t)e * p.F + f) * p.red;
+    const __nv_bfloat16* x = p.x + r * p.red;
+    float s = 0.f;
+    for (int k = 0; k < p.red; k += 2) {
+        const uint32_t a = *reinterpret_cast<const uint32_t*>(x + k), b = *reinterpret_cast<const uint32_t*>(w + k);
+        s = fmaf(bf16_lo(a), bf16_lo(b), s);
+        s = fmaf(bf16_hi(a), bf16_hi(b), s);
+    }
+    const int id = p.lora.adapter[r];
+    if (id >= 0 && id < p.lora.L) {
+        const __nv_bfloat16* u = p.lora.u + r * p.lora.R16;
+        const __nv_bfloat16* b = p.lora.B + (((size_t)id * p.seg.E + e) * p.F + f) * p.lora.R;
+        for (int j = 0; j < p.lora.R; ++j) s = fmaf(__bfloat162float(u[j]), __bfloat162float(b[j]), s);
+    }
+    return s;
+}
+
+__device__ __forceinline__ bool not_finite(uint32_t bits) { return (bits & 0x7f800000u) == 0x7f800000u; }
+
+template <int OP, bool OUT16, int W, bool LORA>
+__global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
     grouped_tc_kernel(const __grid_constant__ Maps maps, const Params p) {
-    using CF = Cfg<OP, OUT16>;
+    using CF = Cfg<OP, OUT16, W, LORA>;
     constexpr bool WGRAD = CF::WGRAD;
+    constexpr int NST = CF::NST, STAGE = CF::STAGE;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + NST * STAGE);
@@ -171,7 +217,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
             ptx::mbar_init(&ctrl->full[s], 1);
             ptx::mbar_init(&ctrl->empty[s], 1);
             ptx::mbar_init(&ctrl->land[s], 1);
-            ptx::mbar_init(&ctrl->ready[s], 2);
+            ptx::mbar_init(&ctrl->ready[s], 2 * (CF::AUX_WARPS > 0 ? CF::AUX_WARPS : 1));
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&ctrl->tfull[b], 1);
@@ -191,7 +237,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
         build_segments(&ctrl->seg, p.seg, BN, leader && cluster == 0 ? p.status : nullptr);
         __syncwarp();
         if (lane == 0) {
-            const int nf = (p.F + 2 * BM - 1) / (2 * BM);
+            const int nf = (p.F + CF::PAIR_F - 1) / CF::PAIR_F;
             const bool ok = ctrl->seg.total == ctrl->seg.base[p.seg.E];
             ctrl->total = !ok ? 0 : WGRAD ? p.seg.E * nf * ((p.C + BN - 1) / BN) : ctrl->seg.total * nf;
         }
@@ -213,28 +259,30 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
             uint32_t armed = 0, armed_phase = 0, tail = 0, tail_phase = 0;   // bits per stage
             bool aborted = false;
             for (int tile = cluster; tile < total && !aborted; tile += nclusters) {
-                const Tile t = decode<WGRAD>(ctrl, p, tile);
+                const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
                 const int fa = t.f0 + (int)rank * BM;
                 const int half = t.nn / 2;
                 const int cb = t.c0 + (int)rank * half;
                 const int box = WGRAD ? 0 : box_of(half);
                 const int bboxes = WGRAD ? (half + BOX - 1) / BOX : 1;
-                const uint32_t bytes = A_BYTES + (WGRAD ? bboxes * (int)MN_LBO : (16 << box) * BK * 2);
+                const uint32_t bytes = W * A_BYTES + (WGRAD ? bboxes * (int)MN_LBO : (16 << box) * BK * 2);
                 for (int kb = 0; kb < t.nkb; ++kb) {
                     if (!ptx::mbar_wait(&ctrl->empty[stage], phase ^ 1u, wc)) {
                         aborted = true;
                         break;
                     }
                     uint8_t* sa = smem + stage * STAGE;
-                    uint8_t* sb = sa + A_BYTES;
+                    uint8_t* sb = sa + W * A_BYTES;
                     const int k = kb * BK;
                     if (WGRAD && kb == t.nkb - 1 && (t.rows & 15) != 0) {
                         // the segment's last block: this CTA's own barrier, the clearing warp goes on from there
                         ptx::mbar_arrive_expect_tx(&ctrl->land[stage], bytes);
                         if (leader) ptx::mbar_arrive(&ctrl->full[stage]);
                         uint64_t* bar = &ctrl->land[stage];
-                        ptx::tma_load_2d(sa, &maps.a, bar, fa, t.row0 + k, pol);
-                        ptx::tma_load_2d(sa + MN_LBO, &maps.a, bar, fa + BOX, t.row0 + k, pol);
+#pragma unroll
+                        for (int h = 0; h < 2 * W; ++h)
+                            ptx::tma_load_2d(sa + h * MN_LBO, &maps.a, bar, fa + (h >> 1) * 2 * BM + (h & 1) * BOX,
+                                             t.row0 + k, pol);
                         for (int h = 0; h < bboxes; ++h)
                             ptx::tma_load_2d(sb + h * MN_LBO, &maps.b[0], bar, cb + h * BOX, t.row0 + k, pol);
                         tail |= 1u << stage;
@@ -242,16 +290,22 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
                         const uint32_t bar = ptx::map_to_rank(ptx::smem_addr(&ctrl->full[stage]), 0);
                         if (leader) ptx::mbar_arrive_expect_tx(&ctrl->full[stage], 2 * bytes);
                         if (WGRAD) {
-                            ptx::tma_load_2d_pair(sa, &maps.a, bar, fa, t.row0 + k, pol);
-                            ptx::tma_load_2d_pair(sa + MN_LBO, &maps.a, bar, fa + BOX, t.row0 + k, pol);
+#pragma unroll
+                            for (int h = 0; h < 2 * W; ++h)
+                                ptx::tma_load_2d_pair(sa + h * MN_LBO, &maps.a, bar,
+                                                      fa + (h >> 1) * 2 * BM + (h & 1) * BOX, t.row0 + k, pol);
                             for (int h = 0; h < bboxes; ++h)
                                 ptx::tma_load_2d_pair(sb + h * MN_LBO, &maps.b[0], bar, cb + h * BOX, t.row0 + k, pol);
                         } else {
                             if (CF::A_MN) {
-                                ptx::tma_load_3d_pair(sa, &maps.a, bar, fa, k, t.e, pol);
-                                ptx::tma_load_3d_pair(sa + MN_LBO, &maps.a, bar, fa + BOX, k, t.e, pol);
+#pragma unroll
+                                for (int h = 0; h < 2 * W; ++h)
+                                    ptx::tma_load_3d_pair(sa + h * MN_LBO, &maps.a, bar,
+                                                          fa + (h >> 1) * 2 * BM + (h & 1) * BOX, k, t.e, pol);
                             } else {
-                                ptx::tma_load_3d_pair(sa, &maps.a, bar, k, fa, t.e, pol);
+#pragma unroll
+                                for (int h = 0; h < W; ++h)
+                                    ptx::tma_load_3d_pair(sa + h * A_BYTES, &maps.a, bar, k, fa + h * 2 * BM, t.e, pol);
                             }
                             ptx::tma_load_2d_pair(sb, &maps.b[box], bar, k, cb, pol);
                         }
@@ -263,6 +317,32 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
                     if (++stage == NST) {
                         stage = 0;
                         phase ^= 1u;
+                    }
+                }
+                if (LORA && !aborted) {
+                    const int slices = tile_slices(p.lora, t.col_tile), per = p.lora.R16 / SLICE;
+                    const int32_t* list = p.lora.tile_list + (size_t)t.col_tile * BN;
+                    for (int s0 = 0; s0 < slices; s0 += SLICES) {
+                        if (!ptx::mbar_wait(&ctrl->empty[stage], phase ^ 1u, wc)) {
+                            aborted = true;
+                            break;
+                        }
+                        const int n = min(SLICES, slices - s0);
+                        const uint32_t bar = ptx::map_to_rank(ptx::smem_addr(&ctrl->full[stage]), 0);
+                        if (leader) ptx::mbar_arrive_expect_tx(&ctrl->full[stage], 2 * n * W * SLICE_BYTES);
+                        for (int i = 0; i < n; ++i) {
+                            const int z = list[(s0 + i) / per] * p.seg.E + t.e, k = (s0 + i) % per * SLICE;
+#pragma unroll
+                            for (int h = 0; h < W; ++h)
+                                ptx::tma_load_3d_pair(smem + stage * STAGE + h * A_BYTES + i * SLICE_BYTES, &maps.l, bar,
+                                                      k, fa + h * 2 * BM, z, pol);
+                        }
+                        armed |= 1u << stage;
+                        armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+                        if (++stage == NST) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
                 }
             }
@@ -287,10 +367,12 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
             uint32_t hand_phase = 0;   // per stage: phase of ready[]
             bool issued = false, aborted = false;
             for (int tile = cluster; tile < total && !aborted; tile += nclusters) {
-                const Tile t = decode<WGRAD>(ctrl, p, tile);
+                const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
                 const uint32_t idesc = ptx::idesc_bf16_f32(2 * BM, t.nn, CF::A_MN, CF::B_MN);
                 uint32_t d_tmem = 0;
-                for (int kb = 0; kb < t.nkb; ++kb) {
+                const int aslices = LORA ? tile_slices(p.lora, t.col_tile) : 0;
+                const int nblk = t.nkb + (aslices + SLICES - 1) / SLICES;
+                for (int kb = 0; kb < nblk; ++kb) {
                     const bool first = OUT16 ? kb == 0 : kb % CHUNK == 0;   // of an accumulator
                     bool ok = true;
                     if (first) {
@@ -307,21 +389,41 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
                             hand_phase ^= 1u << stage;
                         }
                     }
+                    const bool adapters = LORA && kb >= t.nkb;
+                    if (adapters && ok) {
+                        ok = ptx::mbar_wait_cluster(&ctrl->ready[stage], hand_phase >> stage & 1, wc);
+                        hand_phase ^= 1u << stage;
+                    }
                     if (!ok) {
                         aborted = true;
                         break;
                     }
                     ptx::tc_fence_after_sync();
                     const uint32_t a0 = ptx::smem_addr(smem + stage * STAGE);
-                    const uint32_t b0 = a0 + A_BYTES;
+                    const uint32_t b0 = a0 + W * A_BYTES;
+                    if (adapters) {
+                        const int n = min(SLICES, aslices - (kb - t.nkb) * SLICES);
+                        const uint32_t ldesc = ptx::idesc_bf16_f32(2 * BM, t.nn);
+                        for (int i = 0; i < n; ++i)
+#pragma unroll
+                            for (int h = 0; h < W; ++h)
+                                ptx::tc_mma_bf16_pair(d_tmem + h * BN,
+                                                      ptx::desc_kmajor_sw32(a0 + h * A_BYTES + i * SLICE_BYTES),
+                                                      ptx::desc_kmajor_sw32(b0 + i * SLICE_BYTES), ldesc,
+                                                      !(first && i == 0));
+                    }
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk) {
-                        if (WGRAD && kk >= slices) break;
-                        const uint64_t da = CF::A_MN ? ptx::desc_mnmajor_sw128(a0 + kk * 2048, MN_LBO, MN_SBO)
-                                                     : ptx::desc_kmajor_sw128(a0 + kk * 32);
+                        if ((WGRAD && kk >= slices) || adapters) break;
                         const uint64_t db = CF::B_MN ? ptx::desc_mnmajor_sw128(b0 + kk * 2048, MN_LBO, MN_SBO)
                                                      : ptx::desc_kmajor_sw128(b0 + kk * 32);
-                        ptx::tc_mma_bf16_pair(d_tmem, da, db, idesc, !(first && kk == 0));
+#pragma unroll
+                        for (int h = 0; h < W; ++h) {
+                            const uint32_t ah = a0 + h * A_BYTES;
+                            const uint64_t da = CF::A_MN ? ptx::desc_mnmajor_sw128(ah + kk * 2048, MN_LBO, MN_SBO)
+                                                         : ptx::desc_kmajor_sw128(ah + kk * 32);
+                            ptx::tc_mma_bf16_pair(d_tmem + h * BN, da, db, idesc, !(first && kk == 0));
+                        }
                     }
                     ptx::tc_commit_pair_multicast(&ctrl->empty[stage], 0x3);
                     issued = true;
@@ -329,10 +431,12 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
                         stage = 0;
                         phase ^= 1u;
                     }
-                    if (kb == t.nkb - 1 || (!OUT16 && kb % CHUNK == CHUNK - 1)) {
+                    if (kb == nblk - 1 || (!OUT16 && kb % CHUNK == CHUNK - 1)) {
                         ptx::tc_commit_pair_multicast(&ctrl->tfull[acc], 0x3);
-                        acc ^= 1;
-                        if (acc == 0) acc_phase ^= 1u;
+                        if (++acc == CF::ACCS) {
+                            acc = 0;
+                            acc_phase ^= 1u;
+                        }
                     }
                 }
             }
@@ -348,80 +452,127 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
         uint32_t acc_phase = 0;
         bool ok = true;
         for (int tile = cluster; tile < total && ok; tile += nclusters) {
-            const Tile t = decode<WGRAD>(ctrl, p, tile);
-            const int f = t.f0 + (int)rank * BM + q * 32 + lane;
-            const size_t row0 = WGRAD ? (size_t)t.e * p.C + t.c0 : (size_t)t.c0;
+            const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
+            // groups of four warps: block of features, then part of the columns
+            constexpr int PARTS = BN / CF::COLS;
+            const int blk = (warp - 2) / 4 / PARTS, c0 = (warp - 2) / 4 % PARTS * CF::COLS;
+            const int f = t.f0 + blk * 2 * BM + (int)rank * BM + q * 32 + lane;
+            const size_t row0 = (WGRAD ? (size_t)t.e * p.C : (size_t)0) + t.c0 + c0;
+            const int ncol = min(CF::COLS, t.nn - c0);   // a multiple of 32, or none (<= 0)
+            const int aslices = LORA ? tile_slices(p.lora, t.col_tile) : 0;
+            if (WGRAD && t.nkb == 0) {
+                // a segment without rows: nothing was accumulated, the gradient is zero
+                for (int i = 0; f < p.F && i < min(ncol, t.valid - c0); ++i) {
+                    if (OUT16) static_cast<__nv_bfloat16*>(p.out)[(row0 + i) * p.F + f] = __float2bfloat16_rn(0.f);
+                    else static_cast<float*>(p.out)[(row0 + i) * p.F + f] = 0.f;
+                }
+                continue;
+            }
             if (OUT16) {
-                // (no rows in the segment: nothing was accumulated, the sum is zero)
-                if (t.nkb > 0) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->tfull[acc], acc_phase, wc));
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->tfull[acc], acc_phase, wc));
                 if (!ok) break;
                 ptx::tc_fence_after_sync();
-                const uint32_t taddr = tmem_base + (uint32_t)(acc * BN) + ((uint32_t)(q * 32) << 16);
-#pragma unroll 1
-                for (int c = 0; c < t.nn; c += 32) {
-                    uint32_t r[32];
-                    if (t.nkb > 0) {
-                        ptx::tmem_ld_32x32b_x32(taddr + c, r);
-                        ptx::tmem_ld_wait();
-                    } else {
+                // The tile goes to registers first, rounded and packed by column pairs, so that the next
+                // one's MMAs do not wait for the stores.
+                uint32_t v[CF::COLS / 2];
+                const uint32_t taddr = tmem_base + (uint32_t)((acc + blk) * BN + c0) + ((uint32_t)(q * 32) << 16);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) r[i] = 0u;
-                    }
-                    // neighbouring lanes swap one of two columns: the even lane stores features f, f + 1 of
-                    // column i, the odd one features f - 1, f of column i + 1 (F is a multiple of 8)
-                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (f & ~1);
+                for (int c = 0; c < CF::COLS; c += 16) {
+                    if (c >= ncol) break;
+                    uint32_t r[16];
+                    ptx::tmem_ld_32x32b_x16(taddr + c, r);
+                    ptx::tmem_ld_wait();
+                    if (LORA && aslices > 0) {
+                        bool any = false;
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float mine = __uint_as_float(lane & 1 ? r[i + 1] : r[i]);
-                        const float send = __uint_as_float(lane & 1 ? r[i] : r[i + 1]);
-                        const float got = __shfl_xor_sync(0xffffffffu, send, 1);
-                        const uint32_t v = lane & 1 ? pack_bf16x2(got, mine) : pack_bf16x2(mine, got);
-                        const int col = c + i + (lane & 1);
-                        if (col < t.valid && f < p.F)
-                            *reinterpret_cast<uint32_t*>(out + (row0 + col) * (size_t)p.F) = v;
+                        for (int i = 0; i < 16; ++i) any = any || not_finite(r[i]);
+                        if (any) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (not_finite(r[i]) && c0 + c + i < t.valid && f < p.F)
+                                    r[i] = __float_as_uint(recompute(p, t.e, row0 + c + i, f));
+                        }
+                        __syncwarp();
                     }
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2)
+                        v[(c + i) / 2] = pack_bf16x2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
                 }
-                if (t.nkb == 0) continue;
                 // the accumulator is free once every lane's tcgen05.ld has completed
                 ptx::tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
                     ptx::mbar_arrive_cluster_relaxed(ptx::map_to_rank(ptx::smem_addr(&ctrl->tempty[acc]), 0));
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1u;
-            } else {
-                // two warps per lane quarter, each with half of the columns (a multiple of 16)
-                const int half = t.nn / 2, c0 = (warp - 2) / 4 * half;
-                float sum[BN / 2];
+                if (++acc == CF::ACCS) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+                // A lane holds one feature of columns i and i + 1; lanes 0-15 gather pairs of features of column
+                // i, lanes 16-31 of column i + 1, so that neighbouring lanes write neighbouring bytes (with the
+                // columns on alternating lanes every 32-byte sector went to L2 in several pieces: 3.7 times
+                // the output's sectors instead of 1.5).  F is a multiple of 8: pairs are whole.
+                const int hi = lane >> 4, src = 2 * (lane & 15);
+                const int fp = f - lane + src;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (row0 + hi) * p.F + fp;
+                const uint32_t sel = hi ? 0x7632u : 0x5410u;
+                const int cols = (fp < p.F ? t.valid - c0 : 0) - hi;
 #pragma unroll
-                for (int i = 0; i < BN / 2; ++i) sum[i] = 0.f;
-                for (int kb = 0; kb < t.nkb && ok; kb += CHUNK) {
+                for (int c = 0; c < CF::COLS; c += 16) {
+                    if (c >= ncol) break;
+#pragma unroll
+                    for (int i = c; i < c + 16; i += 2) {
+                        const uint32_t a = __shfl_sync(0xffffffffu, v[i / 2], src);
+                        const uint32_t b = __shfl_sync(0xffffffffu, v[i / 2], src + 1);
+                        if (i < cols)
+                            *reinterpret_cast<uint32_t*>(out + (size_t)(i - c) * p.F) = __byte_perm(a, b, sel);
+                    }
+                    out += 16 * (size_t)p.F;
+                    asm volatile("" : "+l"(out));   // one pointer, not one per column, in registers
+                }
+            } else {
+                float sum[CF::COLS];
+#pragma unroll
+                for (int i = 0; i < CF::COLS; ++i) sum[i] = 0.f;
+                const int nblk = t.nkb + (aslices + SLICES - 1) / SLICES;
+                for (int kb = 0; kb < nblk && ok; kb += CHUNK) {
                     ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->tfull[acc], acc_phase, wc));
                     if (!ok) break;
                     ptx::tc_fence_after_sync();
                     const uint32_t taddr = tmem_base + (uint32_t)(acc * BN + c0) + ((uint32_t)(q * 32) << 16);
 #pragma unroll
-                    for (int c = 0; c < BN / 2; c += 16) {
-                        if (c < half) {
-                            uint32_t r[16];
-                            ptx::tmem_ld_32x32b_x16(taddr + c, r);
-                            ptx::tmem_ld_wait();
+                    for (int c = 0; c < CF::COLS; c += 16) {
+                        if (c >= ncol) break;
+                        uint32_t r[16];
+                        ptx::tmem_ld_32x32b_x16(taddr + c, r);
+                        ptx::tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(r[i]);
-                        }
+                        for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(r[i]);
                     }
                     ptx::tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0)
                         ptx::mbar_arrive_cluster_relaxed(ptx::map_to_rank(ptx::smem_addr(&ctrl->tempty[acc]), 0));
-                    acc ^= 1;
-                    if (acc == 0) acc_phase ^= 1u;
+                    if (++acc == CF::ACCS) {
+                        acc = 0;
+                        acc_phase ^= 1u;
+                    }
                 }
                 if (!ok) break;
-                float* out = static_cast<float*>(p.out) + (row0 + c0) * (size_t)p.F + f;
+                float* out = static_cast<float*>(p.out) + row0 * p.F + f;
+                const int valid = f < p.F ? t.valid - c0 : 0;
 #pragma unroll
-                for (int i = 0; i < BN / 2; ++i)
-                    if (i < half && c0 + i < t.valid && f < p.F) out[i * (size_t)p.F] = sum[i];
+                for (int c = 0; c < CF::COLS; c += 16) {
+                    if (c >= ncol) break;
+#pragma unroll
+                    for (int i = c; i < c + 16; ++i)
+                        if (i < valid) {
+                            if (LORA && aslices > 0 && not_finite(__float_as_uint(sum[i])))
+                                sum[i] = recompute(p, t.e, row0 + i, f);
+                            out[(size_t)(i - c) * p.F] = sum[i];
+                        }
+                    out += 16 * (size_t)p.F;
+                    asm volatile("" : "+l"(out));
+                }
             }
         }
     } else if (WGRAD) {
@@ -429,7 +580,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
         int block = 0;             // blocks through the ring so far
         uint32_t land_phase = 0;   // per stage
         for (int tile = cluster; tile < total; tile += nclusters) {
-            const Tile t = decode<WGRAD>(ctrl, p, tile);
+            const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
             block += t.nkb;
             if ((t.rows & 15) == 0) continue;
             const int stage = (block - 1) % NST;
@@ -440,13 +591,74 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
             // rows of the block that lie in its last 16-row slice behind the segment: 128 bytes a row and box
             const int r0 = (t.rows - 1) % BK + 1, r1 = (r0 + 15) / 16 * 16;
             uint8_t* base = smem + stage * STAGE;
-            for (int i = lane; i < (r1 - r0) * 4 * 8; i += 32) {
-                const int v = i & 7, box = (i >> 3) & 3, r = r0 + (i >> 5);
+            constexpr int BOXES = 2 * W + 2;
+            for (int i = lane; i < (r1 - r0) * BOXES * 8; i += 32) {
+                const int v = i & 7, box = (i >> 3) % BOXES, r = r0 + (i >> 3) / BOXES;
                 *reinterpret_cast<uint4*>(base + box * (int)MN_LBO + r * 128 + v * 16) = make_uint4(0, 0, 0, 0);
             }
             ptx::fence_proxy_async();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_addr(&ctrl->ready[stage]), 0));
+        }
+    } else if (LORA) {
+        // ---------------------------------------------------------------- rows of u (both CTAs)
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const int per = p.lora.R16 / SLICE;
+        const int t0 = (warp - 2 - CF::EPI_WARPS) * 32 + lane;   // this thread's rows of the half: t0, t0 + 64
+        for (int tile = cluster; tile < total && ok; tile += nclusters) {
+            const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
+            // every use of a stage is waited for in turn: a parity cannot tell a phase from the one before last
+            for (int kb = 0; kb < t.nkb && ok; ++kb) {
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->empty[stage], phase ^ 1u, wc));
+                if (++stage == NST) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) break;
+            const int slices = tile_slices(p.lora, t.col_tile);
+            const int32_t* list = p.lora.tile_list + (size_t)t.col_tile * BN;
+            int id[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = t0 + 64 * j, col = (int)rank * (t.nn / 2) + r;
+                id[j] = r < t.nn / 2 && col < t.valid ? p.lora.adapter[(size_t)t.c0 + col] : -1;
+            }
+            for (int s0 = 0; s0 < slices && ok; s0 += SLICES) {
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->empty[stage], phase ^ 1u, wc));
+                if (!ok) break;
+                const int n = min(SLICES, slices - s0);
+                uint8_t* sb = smem + stage * STAGE + W * A_BYTES;
+                for (int i = 0; i < n; ++i) {
+                    const int a = list[(s0 + i) / per], k = (s0 + i) % per * SLICE;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int r = t0 + 64 * j;
+                        if (r >= t.nn / 2) continue;
+                        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+                        if (id[j] == a) {
+                            const uint4* u = reinterpret_cast<const uint4*>(
+                                p.lora.u + ((size_t)t.c0 + (int)rank * (t.nn / 2) + r) * p.lora.R16 + k);
+                            lo = u[0];
+                            hi = u[1];
+                        }
+                        // 32-byte swizzle: the two 16-byte halves of a row change places every four rows
+                        uint8_t* row = sb + i * SLICE_BYTES + r * 32;
+                        const int x = (r >> 2 & 1) * 16;
+                        *reinterpret_cast<uint4*>(row + x) = lo;
+                        *reinterpret_cast<uint4*>(row + (16 ^ x)) = hi;
+                    }
+                }
+                ptx::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_addr(&ctrl->ready[stage]), 0));
+                if (++stage == NST) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
         }
     }
 
@@ -459,12 +671,21 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16>::THREADS, 1)
     }
 }
 
-template <int OP, bool OUT16>
-cudaError_t launch(const GroupedArgs& a, const Maps& maps, const Params& p, long long tiles, cudaStream_t s) {
-    using CF = Cfg<OP, OUT16>;
+// Wide tiles (512 features) move a quarter fewer operand bytes per MMA through shared memory, which
+// bounds the narrow ones (8192 x 14336 x 4096: mm 796 -> 709 us, dgrad 892 -> 697, wgrad to bf16 988 -> 745), but
+// have one accumulator: for outputs of at least two waves of them, and where they waste no more than
+// an eighth of the features.  (E = 1, 205 rows, 4096 features: 135 us narrow, 152 wide.)
+bool wide(const Params& p, long long cols, int pairs) {
+    const long long nf = (p.F + 511) / 512;
+    return cols * nf >= 2LL * pairs && nf * 512 * 8 <= (long long)p.F * 9;
+}
+
+template <int OP, bool OUT16, int W, bool LORA = false>
+cudaError_t launch(const GroupedArgs& a, const Maps& maps, const Params& p, long long col_tiles, cudaStream_t s) {
+    using CF = Cfg<OP, OUT16, W, LORA>;
     static PerDeviceOnce attr;
     cudaError_t e = attr.run([] {
-        return cudaFuncSetAttribute(grouped_tc_kernel<OP, OUT16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(grouped_tc_kernel<OP, OUT16, W, LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     CF::SMEM);
     });
     if (e != cudaSuccess) return e;
@@ -486,38 +707,70 @@ cudaError_t launch(const GroupedArgs& a, const Maps& maps, const Params& p, long
         q.gridDim = dim3(2 * 74);
         q.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, grouped_tc_kernel<OP, OUT16>, &q) != cudaSuccess || n <= 0) {
+        if (cudaOccupancyMaxActiveClusters(&n, grouped_tc_kernel<OP, OUT16, W, LORA>, &q) != cudaSuccess || n <= 0) {
             cudaGetLastError();
             n = (a.num_sms > 0 ? a.num_sms : 148) / 2;
         }
         return n;
     });
+    const long long tiles = col_tiles * ((p.F + CF::PAIR_F - 1) / CF::PAIR_F);
     cfg.gridDim = dim3((unsigned)(2 * (tiles < most ? (tiles > 0 ? tiles : 1) : most)));
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, grouped_tc_kernel<OP, OUT16>, maps, p);
+    e = cudaLaunchKernelEx(&cfg, grouped_tc_kernel<OP, OUT16, W, LORA>, maps, p);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// [L * E][N][R] bf16: boxes of 16 of the rank x 128 features, 32-byte swizzle
+bool map_adapters(CUtensorMap* m, const GroupedArgs& a) {
+    const EncodeTiledFn fn = tensor_map_encoder();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)a.R, (cuuint64_t)a.N, (cuuint64_t)a.L * a.seg.E};
+    cuuint64_t strides[2] = {(cuuint64_t)a.R * 2, (cuuint64_t)a.R * a.N * 2};
+    cuuint32_t box[3] = {SLICE, BM, 1}, es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.B), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int OP>
 cudaError_t launch_op(const GroupedArgs& a, cudaStream_t s) {
     const int M = a.seg.M, E = a.seg.E, N = a.N, K = a.K;
-    Params p{a.seg, OP == kGroupedMm ? N : K, N, OP == kGroupedMm ? K : N, a.out, a.status, a.wait_ns};
+    Params p{};
+    p.seg = a.seg;
+    p.F = OP == kGroupedMm ? N : K;
+    p.C = N;
+    p.red = OP == kGroupedMm ? K : N;
+    p.out = a.out;
+    p.status = a.status;
+    p.wait_ns = a.wait_ns;
+    p.f_fast = K <= N;
     Maps m;
     bool ok;
-    long long tiles = (p.F + 2 * BM - 1) / (2 * BM);
+    long long cols;   // upper bound of the tiles along the columns
     if (OP == kGroupedWgrad) {
         ok = map_matrix(&m.a, a.other, M, K, BOX, BK) && map_matrix(&m.b[0], a.rows, M, N, BOX, BK);
         for (int i = 1; i < 4; ++i) m.b[i] = m.b[0];
-        tiles *= (long long)E * ((N + BN - 1) / BN);
+        cols = (long long)E * ((N + BN - 1) / BN);
     } else {
         ok = OP == kGroupedMm ? map_expert_weights(&m.a, a.other, E, N, K, BK, BM)
                               : map_expert_weights(&m.a, a.other, E, N, K, BOX, BK);
         for (int i = 0; i < 4; ++i) ok = ok && map_matrix(&m.b[i], a.rows, M, p.red, BK, 16 << i);
-        const long long tok = (long long)M / BN + E;
-        tiles *= tok < M ? tok : M;   // a segment with rows has at least one
+        cols = (long long)M / BN + E;
+        if (cols > M) cols = M;   // a segment with rows has at least one
     }
     if (!ok) return cudaErrorInvalidValue;
-    return a.out16 ? launch<OP, true>(a, m, p, tiles, s) : launch<OP, false>(a, m, p, tiles, s);
+    if (OP == kGroupedMm && a.A) {
+        p.lora = lora_view(a);
+        p.x = static_cast<const __nv_bfloat16*>(a.rows);
+        p.W = static_cast<const __nv_bfloat16*>(a.other);
+        if (!map_adapters(&m.l, a)) return cudaErrorInvalidValue;
+        if (!a.out16) return launch<kGroupedMm, false, 1, true>(a, m, p, cols, s);
+        return wide(p, cols, (a.num_sms > 0 ? a.num_sms : 148) / 2) ? launch<kGroupedMm, true, 2, true>(a, m, p, cols, s)
+                             : launch<kGroupedMm, true, 1, true>(a, m, p, cols, s);
+    }
+    m.l = m.a;
+    if (!a.out16) return launch<OP, false, 1>(a, m, p, cols, s);
+    return wide(p, cols, (a.num_sms > 0 ? a.num_sms : 148) / 2) ? launch<OP, true, 2>(a, m, p, cols, s) : launch<OP, true, 1>(a, m, p, cols, s);
 }
 
 }  // namespace

@@ -127,10 +127,13 @@ def test_adapters_stay_apart(moe, counts):
     assert not out[ids == 2].isfinite().any()
     keep = (ids == 0) | (ids == 3)
     assert out[keep].isfinite().all()
-    B0 = B.clone()
-    A0 = A.clone()
-    A0[1], B0[2] = 0, 0
-    assert torch.equal(out[keep], moe.moe_grouped_lora(x, W, off, A0, B0, scale, ids)[keep])
+    # The kept rows hold their own terms alone.  Not compared bit for bit with a clean batch: where a
+    # neighbour's infinity meets a zero in the tensor cores' sum, the output is summed again in another
+    # order.  Either order is within check's bound of the exact value: n + 8 roundings of at most an ulp.
+    ids = torch.where(keep, ids, torch.full_like(ids, -1))
+    A[1], B[2] = 0, 0
+    out[~keep] = moe.moe_grouped_lora(x, W, off, A, B, scale, ids)[~keep]
+    _verify(out, counts, starts, x, W, A, B, scale, ids)
 
 
 @pytest.mark.parametrize("counts", [[5, 4], [200, 90]], ids=str)
