@@ -95,7 +95,7 @@ constexpr int MAX_STAGES = 6;
 struct Ctrl {
     uint64_t full[MAX_STAGES];     // leader: both CTAs' bytes of a stage landed
     uint64_t empty[MAX_STAGES];    // each CTA: the MMAs that read a stage are done
-    uint64_t land[MAX_STAGES];     // wgrad: this CTA's bytes of a segment's last block landed
+    uint64_t land[MAX_STAGES];     // wgrad: this CTA's bytes of a segment's last block landed; adapters: stage free
     uint64_t ready[MAX_STAGES];    // leader: both CTAs prepared the stage by hand
     uint64_t tfull[2];      // each CTA: accumulator b holds a finished tile
     uint64_t tempty[2];     // leader: both CTAs' epilogues released accumulator b
@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                             aborted = true;
                             break;
                         }
+                        ptx::mbar_arrive(&ctrl->land[stage]);   // the stage is free: u's warps may write it
                         const int n = min(SLICES, slices - s0);
                         const uint32_t bar = ptx::map_to_rank(ptx::smem_addr(&ctrl->full[stage]), 0);
                         if (leader) ptx::mbar_arrive_expect_tx(&ctrl->full[stage], 2 * n * W * SLICE_BYTES);
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
         }
     } else if (WGRAD) {
         // ---------------------------------------------------------------- ends of segments (both CTAs)
-        int block = 0;             // blocks through the ring so far
+        unsigned block = 0;        // blocks through the ring so far
         uint32_t land_phase = 0;   // per stage
         for (int tile = cluster; tile < total; tile += nclusters) {
             const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
@@ -602,62 +603,73 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
         }
     } else if (LORA) {
         // ---------------------------------------------------------------- rows of u (both CTAs)
-        int stage = 0;
-        uint32_t phase = 0;
+        // They follow the producer's word (land), not the ring's own barriers: a parity can neither tell a
+        // phase from the one before last nor from the one after next, and the MMAs run through a tile's other
+        // blocks without these warps.
+        unsigned block = 0;        // blocks through the ring so far
+        uint32_t land_phase = 0;   // per stage
         bool ok = true;
         const int per = p.lora.R16 / SLICE;
         const int t0 = (warp - 2 - CF::EPI_WARPS) * 32 + lane;   // this thread's rows of the half: t0, t0 + 64
         for (int tile = cluster; tile < total && ok; tile += nclusters) {
             const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
-            // every use of a stage is waited for in turn: a parity cannot tell a phase from the one before last
-            for (int kb = 0; kb < t.nkb && ok; ++kb) {
-                ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->empty[stage], phase ^ 1u, wc));
-                if (++stage == NST) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-            if (!ok) break;
             const int slices = tile_slices(p.lora, t.col_tile);
             const int32_t* list = p.lora.tile_list + (size_t)t.col_tile * BN;
+            const int32_t head = lane < slices / per ? list[lane] : -1;   // the list's first 32 adapters
             int id[2];
+            const uint4* u[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int r = t0 + 64 * j, col = (int)rank * (t.nn / 2) + r;
-                id[j] = r < t.nn / 2 && col < t.valid ? p.lora.adapter[(size_t)t.c0 + col] : -1;
+                const bool live = r < t.nn / 2 && col < t.valid;
+                id[j] = live ? p.lora.adapter[(size_t)t.c0 + col] : -1;
+                u[j] = reinterpret_cast<const uint4*>(p.lora.u + ((size_t)t.c0 + (live ? col : 0)) * p.lora.R16);
             }
-            for (int s0 = 0; s0 < slices && ok; s0 += SLICES) {
-                ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->empty[stage], phase ^ 1u, wc));
-                if (!ok) break;
+            // the rows' part of four slices: read ahead of the wait for the stage
+            uint4 v[SLICES][2][2];
+            auto fetch = [&](int s0) {
                 const int n = min(SLICES, slices - s0);
+#pragma unroll
+                for (int i = 0; i < SLICES; ++i) {
+                    const int k = (s0 + i) / per;
+                    const int h = __shfl_sync(0xffffffffu, head, k & 31);
+                    const int a = i >= n ? -2 : k < 32 ? h : list[k];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        v[i][j][0] = v[i][j][1] = make_uint4(0, 0, 0, 0);
+                        if (id[j] == a) {
+                            v[i][j][0] = u[j][2 * ((s0 + i) % per)];
+                            v[i][j][1] = u[j][2 * ((s0 + i) % per) + 1];
+                        }
+                    }
+                }
+            };
+            if (slices > 0) fetch(0);
+            block += t.nkb;
+            for (int s0 = 0; s0 < slices; s0 += SLICES, ++block) {
+                const int stage = block % NST;
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->land[stage], land_phase >> stage & 1, wc));
+                if (!ok) break;
+                land_phase ^= 1u << stage;
                 uint8_t* sb = smem + stage * STAGE + W * A_BYTES;
-                for (int i = 0; i < n; ++i) {
-                    const int a = list[(s0 + i) / per], k = (s0 + i) % per * SLICE;
+#pragma unroll
+                for (int i = 0; i < SLICES; ++i) {
+                    if (i >= slices - s0) break;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int r = t0 + 64 * j;
                         if (r >= t.nn / 2) continue;
-                        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-                        if (id[j] == a) {
-                            const uint4* u = reinterpret_cast<const uint4*>(
-                                p.lora.u + ((size_t)t.c0 + (int)rank * (t.nn / 2) + r) * p.lora.R16 + k);
-                            lo = u[0];
-                            hi = u[1];
-                        }
                         // 32-byte swizzle: the two 16-byte halves of a row change places every four rows
                         uint8_t* row = sb + i * SLICE_BYTES + r * 32;
                         const int x = (r >> 2 & 1) * 16;
-                        *reinterpret_cast<uint4*>(row + x) = lo;
-                        *reinterpret_cast<uint4*>(row + (16 ^ x)) = hi;
+                        *reinterpret_cast<uint4*>(row + x) = v[i][j][0];
+                        *reinterpret_cast<uint4*>(row + (16 ^ x)) = v[i][j][1];
                     }
                 }
                 ptx::fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_addr(&ctrl->ready[stage]), 0));
-                if (++stage == NST) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+                if (s0 + SLICES < slices) fetch(s0 + SLICES);
             }
         }
     }

@@ -3,24 +3,34 @@
 // takes no part), rounded once to bf16, the operand type of the second half
 // y_r = W_e x_r + B_{a,e} u_r (grouped_tc.cu).
 //
-// A block takes a window of a segment's rows (64, or 16 where that gives too few
-// windows for the SMs), finds the adapters that occur in it and, for each, gathers
-// its rows in groups of 16 for mma.m16n8k16: x's rows are the 16 rows, A's ranks the
-// columns.  Both are read from global memory straight into fragments, 16 bytes a
-// lane: the k order inside a 32-wide step is permuted the same way for both sides.  The
-// 8 warps interleave over the reduction and add their partial sums in a fixed order
-// through shared memory.  What bounds it is reading x and the adapters once per window.
+// A cluster takes a window of 64 rows of a segment, finds the adapters that occur in
+// it, and multiplies the window with 64 rank columns at a time (a column: one rank of
+// one of these adapters), so that short adapters share a pass over x.  Each
+// output keeps only the columns of its own row's adapter.  The CTAs of the cluster split
+// the reduction and add their partial sums through distributed shared memory, in
+// CTA order.  Operands go through a 4-stage cp.async ring (64 of the reduction a stage,
+// 128-byte rows with their 16-byte chunks permuted by row) into ldmatrix and
+// mma.m16n8k16.  What bounds it is reading x and the adapters once per window; the
+// split is what gives small batches enough loads in flight.
 //
-// Further blocks of the same launch write down, for every column tile of the
+// Further clusters of the same launch write down, for every column tile of the
 // product, the adapters that occur among its rows, each once, in order of first
 // occurrence.
 #include "grouped.cuh"
+#include "ptx_grouped.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int WARPS = 8;
-constexpr int RED_BYTES = 64 * 1024;
+constexpr int THREADS = 256;
+constexpr int WARPS = THREADS / 32;
+constexpr int WIN = 64;                      // rows of a window
+constexpr int COLS = 64;                     // rank columns of a pass
+constexpr int KC = 64;                       // reduction per stage
+constexpr int NST = 4;
+constexpr int TILE_BYTES = WIN * KC * 2;     // 8 KiB, either operand
+constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+constexpr int PITCH = COLS + 4;              // floats of a row of partial sums
 
 struct ShrinkParams {
     const __nv_bfloat16* x;
@@ -29,8 +39,8 @@ struct ShrinkParams {
     LoraView v;
     Segments seg;
     int K;
-    int window;    // rows of a window
-    int windows;   // blocks of the first kind (an upper bound of the windows)
+    int split;     // CTAs of a cluster
+    int windows;   // clusters of the first kind along x (an upper bound of the windows)
     int* status;
 };
 
@@ -38,18 +48,36 @@ struct ShrinkSmem {
     SegTable seg;
     int ids[kColumnTile];
     int list[kColumnTile];
-    int rows[64];
     int warp_n[WARPS];
-    int n, m;
+    int n;
 };
+constexpr int SMEM_BYTES = NST * STAGE_BYTES;   // also holds the partial sums of a pass
+static_assert(WIN * PITCH * 4 <= SMEM_BYTES, "partial sums");
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// 16 bytes to shared memory; zeros where !live (src is then not read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // The distinct ids of ids[0, n), in order of first occurrence, into list; sm->n of them (all threads).
@@ -79,119 +107,115 @@ __device__ __forceinline__ int adapter_of(const ShrinkParams& p, size_t r) {
     return -1;
 }
 
-// NT: tiles of 8 ranks (R <= 8 NT); G: groups of 16 rows at a time.
-template <int NT, int G>
-__global__ void __launch_bounds__(32 * WARPS) lora_shrink_kernel(const ShrinkParams p) {
-    extern __shared__ __align__(16) float red[];   // [WARPS][G * 16][NT * 8]
+__global__ void __launch_bounds__(THREADS) lora_shrink_kernel(const ShrinkParams p) {
+    extern __shared__ __align__(128) uint8_t ring[];
     __shared__ ShrinkSmem sm;
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool lists = (int)blockIdx.x >= p.windows;
-    if (warp == 0) build_segments(&sm.seg, p.seg, lists ? kColumnTile : p.window, p.status);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int unit = blockIdx.x / p.split, part = blockIdx.x % p.split;   // cluster, CTA of the cluster
+    const bool lists = unit >= p.windows;
+    if (lists && (part != 0 || blockIdx.y != 0)) return;
+    if (warp == 0) build_segments(&sm.seg, p.seg, lists ? kColumnTile : WIN, p.status);
     __syncthreads();
-    const int tile = lists ? blockIdx.x - p.windows : blockIdx.x;
-    if (tile >= sm.seg.total) return;
+    const int tile = lists ? unit - p.windows : unit;
+    if (tile >= sm.seg.total) return;   // the whole cluster
     const int e = segment_of(&sm.seg, p.seg.E, tile);
-    const int rows = sm.seg.rows[e], h = lists ? column_tile_height(rows) : p.window;
+    const int rows = sm.seg.rows[e], h = lists ? column_tile_height(rows) : WIN;
     const int r0 = (tile - sm.seg.base[e]) * h, n = min(h, rows - r0);
     const size_t row0 = (size_t)sm.seg.row0[e] + r0;
-    if ((int)threadIdx.x < n) sm.ids[threadIdx.x] = adapter_of(p, row0 + threadIdx.x);
+    if (tid < n) sm.ids[tid] = adapter_of(p, row0 + tid);
     __syncthreads();
     distinct(&sm, n);
-    const int na = sm.n;
     if (lists) {
-        if ((int)threadIdx.x < na) p.v.tile_list[(size_t)tile * kColumnTile + threadIdx.x] = sm.list[threadIdx.x];
-        if (threadIdx.x == 0) p.v.tile_count[tile] = na;
+        if (tid < sm.n) p.v.tile_list[(size_t)tile * kColumnTile + tid] = sm.list[tid];
+        if (tid == 0) p.v.tile_count[tile] = sm.n;
         return;
     }
-    const int R = p.v.R, K = p.K;
-    const int g = lane >> 2, q = lane & 3;
-    for (int i = 0; i < na; ++i) {
-        const int a = sm.list[i];
-        // this adapter's rows of the window, in order (the window has at most 64)
-        if (warp < 2) {
-            const uint32_t b0 = __ballot_sync(0xffffffffu, lane < n && sm.ids[lane] == a);
-            const uint32_t b1 = __ballot_sync(0xffffffffu, lane + 32 < n && sm.ids[lane + 32] == a);
-            const uint32_t mine = warp ? b1 : b0;
-            if (mine >> lane & 1)
-                sm.rows[(warp ? __popc(b0) : 0) + __popc(mine & ((1u << lane) - 1))] = warp * 32 + lane;
-            if (threadIdx.x == 0) sm.m = __popc(b0) + __popc(b1);
+
+    const int R = p.v.R, R16 = p.v.R16, K = p.K;
+    const int ncols = sm.n * R16;
+    const int nk = (K + KC - 1) / KC, kb0 = (int)((long long)nk * part / p.split),
+              kb1 = (int)((long long)nk * (part + 1) / p.split);
+    const uint32_t ring0 = ptx::smem_addr(ring);
+    // loads: thread tid fills chunk tid % 8 of rows tid / 8 and tid / 8 + 32 of either operand
+    const int lrow = tid >> 3, lchunk = tid & 7;
+    // products: warp w takes rows 16 (w / 2), columns 32 (w % 2)
+    const int m0 = warp / 2 * 16, n0 = warp % 2 * 32;
+    for (int c0 = blockIdx.y * COLS; c0 < ncols; c0 += gridDim.y * COLS) {
+        const __nv_bfloat16* src[4];   // rows of x, then rank columns
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = lrow + 32 * j, c = c0 + r;
+            src[j] = r < n ? p.x + (row0 + r) * K + lchunk * 8 : nullptr;
+            const int q = c % R16;
+            src[2 + j] = c < ncols && q < R
+                             ? p.A + (((size_t)sm.list[c / R16] * p.seg.E + e) * R + q) * K + lchunk * 8
+                             : nullptr;
         }
-        __syncthreads();
-        const int m = sm.m;
-        const __nv_bfloat16* Aa = p.A + ((size_t)a * p.seg.E + e) * R * K;
-        const float scale = p.scale[a];
-        for (int m0 = 0; m0 < m; m0 += 16 * G) {
-            float acc[G][NT][4];
+        auto load = [&](int kb) {
+            const uint32_t stage = ring0 + (uint32_t)((kb - kb0) % NST) * STAGE_BYTES;
+            const bool in = kb * KC + lchunk * 8 < K;
 #pragma unroll
-            for (int u = 0; u < G; ++u)
+            for (int j = 0; j < 4; ++j) {
+                const int r = lrow + 32 * (j & 1);
+                const bool live = in && src[j];
+                cp_async16(stage + (j >> 1) * TILE_BYTES + r * 128 + ((lchunk ^ (r & 7)) * 16),
+                           live ? src[j] + (size_t)kb * KC : p.x, live);
+            }
+        };
+        float acc[4][4];
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[u][t][c] = 0.f;
-            const __nv_bfloat16* xr[G][2];
+            for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 #pragma unroll
-            for (int u = 0; u < G; ++u)
+        for (int s = 0; s < NST - 1; ++s) {
+            if (kb0 + s < kb1) load(kb0 + s);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        for (int kb = kb0; kb < kb1; ++kb) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
+            __syncthreads();
+            if (kb + NST - 1 < kb1) load(kb + NST - 1);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            const uint32_t sx = ring0 + (uint32_t)((kb - kb0) % NST) * STAGE_BYTES, sa = sx + TILE_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < KC / 16; ++kk) {
+                uint32_t a[4], b[2][4];
+                const int ar = m0 + (lane & 15), ac = 2 * kk + (lane >> 4);
+                ldmatrix4(a, sx + ar * 128 + ((ac ^ (ar & 7)) * 16));
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int r = m0 + 16 * u + 8 * j + g;
-                    xr[u][j] = r < m ? p.x + (row0 + sm.rows[r]) * K : nullptr;
+                    const int br = n0 + 16 * j + (lane & 7) + (lane >> 4) * 8, bc = 2 * kk + (lane >> 3 & 1);
+                    ldmatrix4(b[j], sa + br * 128 + ((bc ^ (br & 7)) * 16));
                 }
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 2
-            for (int k0 = warp * 32; k0 < K; k0 += WARPS * 32) {
-                const int k = k0 + 8 * q;
-                const bool in = k < K;
-                uint4 bv[NT];
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    bv[t] = in && t * 8 + g < R
-                                ? __ldg(reinterpret_cast<const uint4*>(Aa + (size_t)(t * 8 + g) * K + k))
-                                : zero;
-#pragma unroll
-                for (int u = 0; u < G; ++u) {
-                    if (u > 0 && m0 + 16 * u >= m) break;
-                    const uint4 lo = in && xr[u][0] ? __ldg(reinterpret_cast<const uint4*>(xr[u][0] + k)) : zero;
-                    const uint4 hi = in && xr[u][1] ? __ldg(reinterpret_cast<const uint4*>(xr[u][1] + k)) : zero;
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        mma16816(acc[u][t], lo.x, hi.x, lo.y, hi.y, bv[t].x, bv[t].y);
-                        mma16816(acc[u][t], lo.z, hi.z, lo.w, hi.w, bv[t].z, bv[t].w);
-                    }
-                }
+                for (int i = 0; i < 4; ++i) mma16816(acc[i], a, b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
             }
-            float* mine = red + (size_t)warp * G * 16 * NT * 8;
-#pragma unroll
-            for (int u = 0; u < G; ++u)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        mine[(16 * u + g + 8 * (c >> 1)) * (NT * 8) + t * 8 + 2 * q + (c & 1)] = acc[u][t][c];
-            __syncthreads();
-            for (int o = threadIdx.x; o < G * 16 * NT * 8; o += 32 * WARPS) {
-                const int r = m0 + o / (NT * 8), j = o % (NT * 8);
-                if (r >= m || j >= p.v.R16) continue;
-                float s = 0.f;
-#pragma unroll
-                for (int w = 0; w < WARPS; ++w) s += red[(size_t)w * G * 16 * NT * 8 + o];
-                p.v.u[(row0 + sm.rows[r]) * p.v.R16 + j] = __float2bfloat16_rn(j < R ? s * scale : 0.f);
-            }
-            __syncthreads();
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        float* red = reinterpret_cast<float*>(ring);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                red[(m0 + (lane >> 2) + 8 * (j >> 1)) * PITCH + n0 + 8 * i + 2 * (lane & 3) + (j & 1)] = acc[i][j];
+        ptx::cluster_sync();
+        // CTA `part` finishes rows part, part + split, ...: its columns are those of the row's adapter
+        for (int o = tid; o < (WIN + p.split - 1) / p.split * COLS; o += THREADS) {
+            const int r = o / COLS * p.split + part, c = c0 + o % COLS;
+            if (r >= n || c >= ncols) continue;
+            const int a = sm.list[c / R16];
+            if (sm.ids[r] != a) continue;
+            float s = 0.f;
+            const uint32_t at = ptx::smem_addr(red + r * PITCH + (c - c0));
+            for (int i = 0; i < p.split; ++i) s += ld_cluster(ptx::map_to_rank(at, i));
+            p.v.u[(row0 + r) * R16 + c % R16] = __float2bfloat16_rn(c % R16 < R ? s * p.scale[a] : 0.f);
+        }
+        ptx::cluster_sync();   // the ring is free again, and no CTA exits while its sums are read
     }
-}
-
-template <int NT, int G>
-cudaError_t launch(const ShrinkParams& p, int blocks, cudaStream_t s) {
-    static_assert(WARPS * G * 16 * NT * 8 * 4 <= RED_BYTES, "reduction buffer");
-    static PerDeviceOnce attr;
-    const cudaError_t e = attr.run([] {
-        return cudaFuncSetAttribute(lora_shrink_kernel<NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, RED_BYTES);
-    });
-    if (e != cudaSuccess) return e;
-    return launch_pdl(lora_shrink_kernel<NT, G>, dim3(blocks), dim3(32 * WARPS), RED_BYTES, s, p);
 }
 
 }  // namespace
@@ -206,15 +230,35 @@ cudaError_t launch_lora_shrink(const GroupedArgs& a, cudaStream_t s) {
     p.K = a.K;
     p.status = a.status;
     const int M = a.seg.M, E = a.seg.E, sms = a.num_sms > 0 ? a.num_sms : 148;
-    p.window = M >= 64 * sms ? 64 : 16;
-    const long long w = (long long)M / p.window + E;
-    p.windows = (int)(w < M ? w : M);
-    const long long t = (long long)M / kColumnTile + E;
-    const int blocks = p.windows + (int)(t < M ? t : M);
-    if (a.R <= 16) return launch<2, 4>(p, blocks, s);
-    if (a.R <= 32) return launch<4, 4>(p, blocks, s);
-    if (a.R <= 64) return launch<8, 2>(p, blocks, s);
-    return launch<16, 1>(p, blocks, s);
+    auto tiles = [&](int h) { return (int)((long long)M / h + E < M ? (long long)M / h + E : M); };
+    p.windows = tiles(WIN);
+    // split the reduction while the windows leave SMs idle and every part has at least four stages
+    p.split = 1;
+    while (p.split < 8 && p.windows * p.split <= 2 * sms && (a.K + KC - 1) / KC >= 8 * p.split) p.split *= 2;
+    // passes side by side: as many as a window can have, no more than fill the SMs a few times over
+    const long long most = ((long long)(a.L < WIN ? a.L : WIN) * p.v.R16 + COLS - 1) / COLS;
+    const long long room = 4LL * sms / ((long long)p.windows * p.split) + 1;
+    static PerDeviceOnce attr;
+    cudaError_t e = attr.run([] {
+        return cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = p.split;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)((p.windows + tiles(kColumnTile)) * p.split), (unsigned)(most < room ? most : room));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace moe
