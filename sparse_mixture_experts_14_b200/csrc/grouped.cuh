@@ -121,6 +121,7 @@ struct LoraView {
     int32_t* tile_list;            // [column tiles][256]: the adapters that occur in the tile, each once
     int32_t* tile_count;           // [column tiles]
     int L, R, R16;
+    int box;                       // ranks of a box of B: the widest of 64, 32, 16 that divides R16
 };
 
 inline size_t lora_tiles(int M, int E) { return (size_t)M / kColumnTile + E; }
@@ -138,6 +139,7 @@ inline LoraView lora_view(const GroupedArgs& a) {
     v.L = a.L;
     v.R = a.R;
     v.R16 = (a.R + 15) / 16 * 16;
+    v.box = v.R16 % 64 == 0 ? 64 : v.R16 % 32 == 0 ? 32 : 16;
     return v;
 }
 

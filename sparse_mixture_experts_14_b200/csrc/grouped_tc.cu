@@ -34,9 +34,11 @@
 //
 // Adapters (lora.cu computes u_r = s_a A_{a,e} x_r, bf16): B_{a,e} u_r is more of the
 // same reduction.  For every adapter that occurs among a tile's rows, in slices of 16
-// of its rank, the ring takes 128 x 16 boxes of B_{a,e} (A side, 32-byte swizzle) and,
-// written by two extra warps, the tile's rows of u with zeros in the rows of other
-// adapters (B side): one K = 16 MMA a slice, four slices a stage.  A zero does not
+// of its rank, the ring takes boxes of B_{a,e} (A side) and, written by two extra warps,
+// the tile's rows of u with zeros in the rows of other adapters (B side): one K = 16
+// MMA a slice, four slices a stage.  Boxes are 64, 32 or 16 ranks wide, the widest
+// that divides the padded rank, with the swizzle of that width: TMA's time goes by
+// rows (rank 64 in boxes of 16 cost a prefill 71 us of 413, in boxes of 64 BOXUS).  A zero does not
 // hide an infinity or NaN in another request's adapter, so where the sum is not finite
 // the epilogue computes that output again from its own terms alone.
 //
@@ -67,12 +69,12 @@ constexpr int CHUNK = 512 / BK;            // blocks per accumulator, fp32 outpu
 
 constexpr int SLICE = 16;                   // rank slice of one adapter MMA
 constexpr int SLICES = 4;                   // of a stage
-constexpr int SLICE_BYTES = BM * SLICE * 2; // 4 KiB, either side
+constexpr int SLICE_BYTES = BM * SLICE * 2; // 4 KiB, either side (a box w wide is w / 16 of them)
 
 struct Maps {
     CUtensorMap a;
     CUtensorMap b[4];   // boxes of 16, 32, 64 and 128 rows (mm, dgrad); wgrad: b[0] only
-    CUtensorMap l;      // adapters: B_{a,e}, boxes of 16 x 128 features
+    CUtensorMap l;      // adapters: B_{a,e}, boxes of lora.box x 128 features
 };
 
 struct Params {
@@ -174,11 +176,15 @@ __device__ __forceinline__ int tile_slices(const LoraView& l, int col_tile) {
     return l.tile_count[col_tile] * (l.R16 / SLICE);
 }
 
+// What the TMA's swizzle of rows of 2 box bytes does to row r: its 16-byte chunk c is kept at c ^ swizzle.
+__device__ __forceinline__ int swizzle(int r, int box) { return box == 64 ? r & 7 : box == 32 ? r >> 1 & 3 : r >> 2 & 1; }
+
 // One output from its own terms: x_r W_e^T[f] and, with an adapter, u_r B_{a,e}^T[f].
-__device__ __noinline__ float recompute(const Params& p, int e, size_t r, int f) {
+__device__ __forceinline__ float recompute(const Params& p, int e, size_t r, int f) {
     const __nv_bfloat16* w = p.W + ((size_t)e * p.F + f) * p.red;
     const __nv_bfloat16* x = p.x + r * p.red;
     float s = 0.f;
+#pragma unroll 1
     for (int k = 0; k < p.red; k += 2) {
         const uint32_t a = *reinterpret_cast<const uint32_t*>(x + k), b = *reinterpret_cast<const uint32_t*>(w + k);
         s = fmaf(bf16_lo(a), bf16_lo(b), s);
@@ -188,6 +194,7 @@ __device__ __noinline__ float recompute(const Params& p, int e, size_t r, int f)
     if (id >= 0 && id < p.lora.L) {
         const __nv_bfloat16* u = p.lora.u + r * p.lora.R16;
         const __nv_bfloat16* b = p.lora.B + (((size_t)id * p.seg.E + e) * p.F + f) * p.lora.R;
+#pragma unroll 1
         for (int j = 0; j < p.lora.R; ++j) s = fmaf(__bfloat162float(u[j]), __bfloat162float(b[j]), s);
     }
     return s;
@@ -197,7 +204,7 @@ __device__ __forceinline__ bool not_finite(uint32_t bits) { return (bits & 0x7f8
 
 template <int OP, bool OUT16, int W, bool LORA>
 __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
-    grouped_tc_kernel(const __grid_constant__ Maps maps, const Params p) {
+    grouped_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     using CF = Cfg<OP, OUT16, W, LORA>;
     constexpr bool WGRAD = CF::WGRAD;
     constexpr int NST = CF::NST, STAGE = CF::STAGE;
@@ -265,6 +272,14 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                 const int cb = t.c0 + (int)rank * half;
                 const int box = WGRAD ? 0 : box_of(half);
                 const int bboxes = WGRAD ? (half + BOX - 1) / BOX : 1;
+                // (asked for now, needed behind the last of the other blocks)
+                const int32_t* list = LORA ? p.lora.tile_list + (size_t)t.col_tile * BN : nullptr;
+                const int slices = LORA ? tile_slices(p.lora, t.col_tile) : 0, per = LORA ? p.lora.R16 / SLICE : 1;
+                int z[SLICES];
+                if (LORA) {
+#pragma unroll
+                    for (int i = 0; i < SLICES; ++i) z[i] = list[i / per];
+                }
                 const uint32_t bytes = W * A_BYTES + (WGRAD ? bboxes * (int)MN_LBO : (16 << box) * BK * 2);
                 for (int kb = 0; kb < t.nkb; ++kb) {
                     if (!ptx::mbar_wait(&ctrl->empty[stage], phase ^ 1u, wc)) {
@@ -320,24 +335,28 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                     }
                 }
                 if (LORA && !aborted) {
-                    const int slices = tile_slices(p.lora, t.col_tile), per = p.lora.R16 / SLICE;
-                    const int32_t* list = p.lora.tile_list + (size_t)t.col_tile * BN;
                     for (int s0 = 0; s0 < slices; s0 += SLICES) {
+                        const int n = min(SLICES, slices - s0);
                         if (!ptx::mbar_wait(&ctrl->empty[stage], phase ^ 1u, wc)) {
                             aborted = true;
                             break;
                         }
                         ptx::mbar_arrive(&ctrl->land[stage]);   // the stage is free: u's warps may write it
-                        const int n = min(SLICES, slices - s0);
                         const uint32_t bar = ptx::map_to_rank(ptx::smem_addr(&ctrl->full[stage]), 0);
                         if (leader) ptx::mbar_arrive_expect_tx(&ctrl->full[stage], 2 * n * W * SLICE_BYTES);
-                        for (int i = 0; i < n; ++i) {
-                            const int z = list[(s0 + i) / per] * p.seg.E + t.e, k = (s0 + i) % per * SLICE;
+                        const int step = p.lora.box / SLICE;
+#pragma unroll
+                        for (int i = 0; i < SLICES; ++i) {
+                            if (i >= n) break;
+                            if (i % step != 0) continue;
 #pragma unroll
                             for (int h = 0; h < W; ++h)
                                 ptx::tma_load_3d_pair(smem + stage * STAGE + h * A_BYTES + i * SLICE_BYTES, &maps.l, bar,
-                                                      k, fa + h * 2 * BM, z, pol);
+                                                      (s0 + i) % per * SLICE, fa + h * 2 * BM, z[i] * p.seg.E + t.e,
+                                                      pol);
                         }
+#pragma unroll
+                        for (int i = 0; i < SLICES; ++i) z[i] = list[min(s0 + SLICES + i, slices - 1) / per];
                         armed |= 1u << stage;
                         armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
                         if (++stage == NST) {
@@ -367,78 +386,92 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
             uint32_t acc_phase = 0;
             uint32_t hand_phase = 0;   // per stage: phase of ready[]
             bool issued = false, aborted = false;
+            // Descriptors of the ring's first stage; others differ in the address field alone (16-byte units).
+            // One thread issues every MMA: what it computes per MMA is kept to an addition.
+            const uint32_t ring = ptx::smem_addr(smem);
+            const uint64_t da0 = CF::A_MN ? ptx::desc_mnmajor_sw128(ring, MN_LBO, MN_SBO) : ptx::desc_kmajor_sw128(ring);
+            const uint64_t db0 = CF::B_MN ? ptx::desc_mnmajor_sw128(ring + W * A_BYTES, MN_LBO, MN_SBO)
+                                          : ptx::desc_kmajor_sw128(ring + W * A_BYTES);
+            constexpr uint32_t A_STEP = (CF::A_MN ? 2048 : 32) / 16, B_STEP = (CF::B_MN ? 2048 : 32) / 16;
+            // wait for block kb's accumulator (where it opens one) and operands
+            uint32_t d_tmem = 0;
+            auto open = [&](bool first) {
+                if (first) {
+                    if (!ptx::mbar_wait(&ctrl->tempty[acc], acc_phase ^ 1u, wc)) return false;
+                    d_tmem = tmem_base + (uint32_t)(acc * BN);
+                }
+                return ptx::mbar_wait(&ctrl->full[stage], phase, wc);
+            };
+            auto by_hand = [&]() {   // the stage was also written by this pair's warps
+                const bool ok = ptx::mbar_wait(&ctrl->ready[stage], hand_phase >> stage & 1, wc);
+                hand_phase ^= 1u << stage;
+                return ok;
+            };
+            auto close = [&](bool last) {
+                ptx::tc_commit_pair_multicast(&ctrl->empty[stage], 0x3);
+                issued = true;
+                if (++stage == NST) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                if (last) {
+                    ptx::tc_commit_pair_multicast(&ctrl->tfull[acc], 0x3);
+                    if (++acc == CF::ACCS) {
+                        acc = 0;
+                        acc_phase ^= 1u;
+                    }
+                }
+            };
             for (int tile = cluster; tile < total && !aborted; tile += nclusters) {
                 const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
                 const uint32_t idesc = ptx::idesc_bf16_f32(2 * BM, t.nn, CF::A_MN, CF::B_MN);
-                uint32_t d_tmem = 0;
                 const int aslices = LORA ? tile_slices(p.lora, t.col_tile) : 0;
-                const int nblk = t.nkb + (aslices + SLICES - 1) / SLICES;
-                for (int kb = 0; kb < nblk; ++kb) {
+                for (int kb = 0; kb < t.nkb; ++kb) {
                     const bool first = OUT16 ? kb == 0 : kb % CHUNK == 0;   // of an accumulator
-                    bool ok = true;
-                    if (first) {
-                        ok = ptx::mbar_wait(&ctrl->tempty[acc], acc_phase ^ 1u, wc);
-                        ptx::tc_fence_after_sync();
-                        d_tmem = tmem_base + (uint32_t)(acc * BN);
-                    }
-                    ok = ok && ptx::mbar_wait(&ctrl->full[stage], phase, wc);
+                    bool ok = open(first);
                     int slices = BK / 16;
                     if (WGRAD && kb == t.nkb - 1) {
                         slices = (t.rows - kb * BK + 15) / 16;
-                        if (ok && (t.rows & 15) != 0) {
-                            ok = ptx::mbar_wait_cluster(&ctrl->ready[stage], hand_phase >> stage & 1, wc);
-                            hand_phase ^= 1u << stage;
-                        }
-                    }
-                    const bool adapters = LORA && kb >= t.nkb;
-                    if (adapters && ok) {
-                        ok = ptx::mbar_wait_cluster(&ctrl->ready[stage], hand_phase >> stage & 1, wc);
-                        hand_phase ^= 1u << stage;
+                        if (ok && (t.rows & 15) != 0) ok = by_hand();
                     }
                     if (!ok) {
                         aborted = true;
                         break;
                     }
                     ptx::tc_fence_after_sync();
-                    const uint32_t a0 = ptx::smem_addr(smem + stage * STAGE);
-                    const uint32_t b0 = a0 + W * A_BYTES;
-                    if (adapters) {
-                        const int n = min(SLICES, aslices - (kb - t.nkb) * SLICES);
-                        const uint32_t ldesc = ptx::idesc_bf16_f32(2 * BM, t.nn);
-                        for (int i = 0; i < n; ++i)
-#pragma unroll
-                            for (int h = 0; h < W; ++h)
-                                ptx::tc_mma_bf16_pair(d_tmem + h * BN,
-                                                      ptx::desc_kmajor_sw32(a0 + h * A_BYTES + i * SLICE_BYTES),
-                                                      ptx::desc_kmajor_sw32(b0 + i * SLICE_BYTES), ldesc,
-                                                      !(first && i == 0));
-                    }
+                    const uint64_t da = da0 + (uint32_t)stage * (STAGE / 16), db = db0 + (uint32_t)stage * (STAGE / 16);
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk) {
-                        if ((WGRAD && kk >= slices) || adapters) break;
-                        const uint64_t db = CF::B_MN ? ptx::desc_mnmajor_sw128(b0 + kk * 2048, MN_LBO, MN_SBO)
-                                                     : ptx::desc_kmajor_sw128(b0 + kk * 32);
+                        if (WGRAD && kk >= slices) break;
 #pragma unroll
-                        for (int h = 0; h < W; ++h) {
-                            const uint32_t ah = a0 + h * A_BYTES;
-                            const uint64_t da = CF::A_MN ? ptx::desc_mnmajor_sw128(ah + kk * 2048, MN_LBO, MN_SBO)
-                                                         : ptx::desc_kmajor_sw128(ah + kk * 32);
-                            ptx::tc_mma_bf16_pair(d_tmem + h * BN, da, db, idesc, !(first && kk == 0));
-                        }
+                        for (int h = 0; h < W; ++h)
+                            ptx::tc_mma_bf16_pair(d_tmem + h * BN, da + h * (A_BYTES / 16) + kk * A_STEP, db + kk * B_STEP,
+                                                  idesc, kk > 0 || !first);
                     }
-                    ptx::tc_commit_pair_multicast(&ctrl->empty[stage], 0x3);
-                    issued = true;
-                    if (++stage == NST) {
-                        stage = 0;
-                        phase ^= 1u;
+                    close((!OUT16 && kb % CHUNK == CHUNK - 1) || (kb == t.nkb - 1 && (!LORA || aslices == 0)));
+                }
+                if (!LORA || aborted) continue;
+                const int box = p.lora.box, step = box / SLICE;
+                const uint64_t la0 = ptx::desc_kmajor(ring, box * 2), lb0 = ptx::desc_kmajor(ring + W * A_BYTES, box * 2);
+                int kb = t.nkb;
+                for (int s0 = 0; s0 < aslices; s0 += SLICES, ++kb) {
+                    const bool first = !OUT16 && kb % CHUNK == 0;
+                    if (!open(first) || !by_hand()) {
+                        aborted = true;
+                        break;
                     }
-                    if (kb == nblk - 1 || (!OUT16 && kb % CHUNK == CHUNK - 1)) {
-                        ptx::tc_commit_pair_multicast(&ctrl->tfull[acc], 0x3);
-                        if (++acc == CF::ACCS) {
-                            acc = 0;
-                            acc_phase ^= 1u;
-                        }
+                    ptx::tc_fence_after_sync();
+                    const int n = min(SLICES, aslices - s0);
+                    const uint64_t la = la0 + (uint32_t)stage * (STAGE / 16), lb = lb0 + (uint32_t)stage * (STAGE / 16);
+                    for (int i = 0; i < n; ++i) {
+                        // box i / step, 32 bytes into its rows for every slice before this one
+                        const uint32_t at = (uint32_t)(i / step * step * SLICE_BYTES + i % step * 32) / 16;
+#pragma unroll
+                        for (int h = 0; h < W; ++h)
+                            ptx::tc_mma_bf16_pair(d_tmem + h * BN, la + h * (A_BYTES / 16) + at, lb + at, idesc,
+                                                  i > 0 || !first);
                     }
+                    close((!OUT16 && kb % CHUNK == CHUNK - 1) || s0 + SLICES >= aslices);
                 }
             }
             if ((aborted || ctrl->abort) && issued) {
@@ -453,17 +486,16 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
         uint32_t acc_phase = 0;
         bool ok = true;
         for (int tile = cluster; tile < total && ok; tile += nclusters) {
-            const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
             // groups of four warps: block of features, then part of the columns
             constexpr int PARTS = BN / CF::COLS;
             const int blk = (warp - 2) / 4 / PARTS, c0 = (warp - 2) / 4 % PARTS * CF::COLS;
-            const int f = t.f0 + blk * 2 * BM + (int)rank * BM + q * 32 + lane;
-            const size_t row0 = (WGRAD ? (size_t)t.e * p.C : (size_t)0) + t.c0 + c0;
-            const int ncol = min(CF::COLS, t.nn - c0);   // a multiple of 32, or none (<= 0)
-            const int aslices = LORA ? tile_slices(p.lora, t.col_tile) : 0;
-            if (WGRAD && t.nkb == 0) {
+            const Tile t0 = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
+            const int ncol = min(CF::COLS, t0.nn - c0);   // a multiple of 32, or none (<= 0)
+            if (WGRAD && t0.nkb == 0) {
                 // a segment without rows: nothing was accumulated, the gradient is zero
-                for (int i = 0; f < p.F && i < min(ncol, t.valid - c0); ++i) {
+                const int f = t0.f0 + blk * 2 * BM + (int)rank * BM + q * 32 + lane;
+                const size_t row0 = (size_t)t0.e * p.C + t0.c0 + c0;
+                for (int i = 0; f < p.F && i < min(ncol, t0.valid - c0); ++i) {
                     if (OUT16) static_cast<__nv_bfloat16*>(p.out)[(row0 + i) * p.F + f] = __float2bfloat16_rn(0.f);
                     else static_cast<float*>(p.out)[(row0 + i) * p.F + f] = 0.f;
                 }
@@ -483,18 +515,6 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                     uint32_t r[16];
                     ptx::tmem_ld_32x32b_x16(taddr + c, r);
                     ptx::tmem_ld_wait();
-                    if (LORA && aslices > 0) {
-                        bool any = false;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) any = any || not_finite(r[i]);
-                        if (any) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (not_finite(r[i]) && c0 + c + i < t.valid && f < p.F)
-                                    r[i] = __float_as_uint(recompute(p, t.e, row0 + c + i, f));
-                        }
-                        __syncwarp();
-                    }
 #pragma unroll
                     for (int i = 0; i < 16; i += 2)
                         v[(c + i) / 2] = pack_bf16x2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
@@ -508,12 +528,27 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                     acc = 0;
                     acc_phase ^= 1u;
                 }
+                // where it goes is worked out only now: the registers were needed
+                asm volatile("" : "+r"(tile));
+                const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
+                const int aslices = LORA ? tile_slices(p.lora, t.col_tile) : 0;
+                const size_t row0 = (WGRAD ? (size_t)t.e * p.C : (size_t)0) + t.c0 + c0;
+                bool odd = false;   // something is not finite: zero times a finite value is zero
+                if (LORA && aslices > 0) {
+                    __nv_bfloat162 t2 = __floats2bfloat162_rn(0.f, 0.f);
+                    const __nv_bfloat162 zero = t2;
+#pragma unroll
+                    for (int i = 0; i < CF::COLS; i += 2)
+                        if (i < ncol) t2 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v[i / 2]), zero, t2);
+                    odd = !(__low2float(t2) == 0.f && __high2float(t2) == 0.f);
+                    odd = __any_sync(0xffffffffu, odd);
+                }
                 // A lane holds one feature of columns i and i + 1; lanes 0-15 gather pairs of features of column
                 // i, lanes 16-31 of column i + 1, so that neighbouring lanes write neighbouring bytes (with the
                 // columns on alternating lanes every 32-byte sector went to L2 in several pieces: 3.7 times
                 // the output's sectors instead of 1.5).  F is a multiple of 8: pairs are whole.
                 const int hi = lane >> 4, src = 2 * (lane & 15);
-                const int fp = f - lane + src;
+                const int fp = t.f0 + blk * 2 * BM + (int)rank * BM + q * 32 + src;
                 __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (row0 + hi) * p.F + fp;
                 const uint32_t sel = hi ? 0x7632u : 0x5410u;
                 const int cols = (fp < p.F ? t.valid - c0 : 0) - hi;
@@ -530,11 +565,26 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                     out += 16 * (size_t)p.F;
                     asm volatile("" : "+l"(out));   // one pointer, not one per column, in registers
                 }
+                if (LORA && odd) {
+                    // every lane goes through what it has just stored
+                    out = static_cast<__nv_bfloat16*>(p.out) + (row0 + hi) * p.F + fp;
+#pragma unroll 1
+                    for (int i = 0; i < min(cols, ncol); i += 2) {
+#pragma unroll 1
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t bits = (uint32_t)__bfloat16_as_ushort(out[(size_t)i * p.F + j]) << 16;
+                            if (not_finite(bits))
+                                out[(size_t)i * p.F + j] = __float2bfloat16_rn(recompute(p, t.e, row0 + hi + i, fp + j));
+                        }
+                    }
+                    __syncwarp();
+                }
             } else {
                 float sum[CF::COLS];
 #pragma unroll
                 for (int i = 0; i < CF::COLS; ++i) sum[i] = 0.f;
-                const int nblk = t.nkb + (aslices + SLICES - 1) / SLICES;
+                const int aslices = LORA ? tile_slices(p.lora, t0.col_tile) : 0;
+                const int nblk = t0.nkb + (aslices + SLICES - 1) / SLICES;
                 for (int kb = 0; kb < nblk && ok; kb += CHUNK) {
                     ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->tfull[acc], acc_phase, wc));
                     if (!ok) break;
@@ -559,6 +609,10 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                     }
                 }
                 if (!ok) break;
+                asm volatile("" : "+r"(tile));
+                const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
+                const int f = t.f0 + blk * 2 * BM + (int)rank * BM + q * 32 + lane;
+                const size_t row0 = (WGRAD ? (size_t)t.e * p.C : (size_t)0) + t.c0 + c0;
                 float* out = static_cast<float*>(p.out) + row0 * p.F + f;
                 const int valid = f < p.F ? t.valid - c0 : 0;
 #pragma unroll
@@ -566,13 +620,22 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                     if (c >= ncol) break;
 #pragma unroll
                     for (int i = c; i < c + 16; ++i)
-                        if (i < valid) {
-                            if (LORA && aslices > 0 && not_finite(__float_as_uint(sum[i])))
-                                sum[i] = recompute(p, t.e, row0 + i, f);
-                            out[(size_t)(i - c) * p.F] = sum[i];
-                        }
+                        if (i < valid) out[(size_t)(i - c) * p.F] = sum[i];
                     out += 16 * (size_t)p.F;
                     asm volatile("" : "+l"(out));
+                }
+                if (LORA && aslices > 0) {
+                    float z = 0.f;   // (zero times a finite value is zero)
+#pragma unroll
+                    for (int i = 0; i < CF::COLS; ++i) z = fmaf(sum[i], 0.f, z);
+                    if (z != 0.f) {
+                        out = static_cast<float*>(p.out) + row0 * p.F + f;
+#pragma unroll 1
+                        for (int i = 0; i < min(valid, ncol); ++i)
+                            if (not_finite(__float_as_uint(out[(size_t)i * p.F])))
+                                out[(size_t)i * p.F] = recompute(p, t.e, row0 + i, f);
+                    }
+                    __syncwarp();
                 }
             }
         }
@@ -599,7 +662,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
             }
             ptx::fence_proxy_async();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_addr(&ctrl->ready[stage]), 0));
+            if (lane == 0) ptx::mbar_arrive_operands(ptx::map_to_rank(ptx::smem_addr(&ctrl->ready[stage]), 0));
         }
     } else if (LORA) {
         // ---------------------------------------------------------------- rows of u (both CTAs)
@@ -609,7 +672,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
         unsigned block = 0;        // blocks through the ring so far
         uint32_t land_phase = 0;   // per stage
         bool ok = true;
-        const int per = p.lora.R16 / SLICE;
+        const int per = p.lora.R16 / SLICE, box = p.lora.box, step = box / SLICE;
         const int t0 = (warp - 2 - CF::EPI_WARPS) * 32 + lane;   // this thread's rows of the half: t0, t0 + 64
         for (int tile = cluster; tile < total && ok; tile += nclusters) {
             const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
@@ -659,16 +722,16 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                     for (int j = 0; j < 2; ++j) {
                         const int r = t0 + 64 * j;
                         if (r >= t.nn / 2) continue;
-                        // 32-byte swizzle: the two 16-byte halves of a row change places every four rows
-                        uint8_t* row = sb + i * SLICE_BYTES + r * 32;
-                        const int x = (r >> 2 & 1) * 16;
-                        *reinterpret_cast<uint4*>(row + x) = v[i][j][0];
-                        *reinterpret_cast<uint4*>(row + (16 ^ x)) = v[i][j][1];
+                        // box i / step, rows of 2 box bytes whose 16-byte chunks are permuted by row as TMA does
+                        const int chunk = i % step * 2, x = swizzle(r, box);
+                        uint8_t* row = sb + i / step * step * SLICE_BYTES + r * 2 * box;
+                        *reinterpret_cast<uint4*>(row + (chunk ^ x) * 16) = v[i][j][0];
+                        *reinterpret_cast<uint4*>(row + ((chunk + 1) ^ x) * 16) = v[i][j][1];
                     }
                 }
                 ptx::fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_addr(&ctrl->ready[stage]), 0));
+                if (lane == 0) ptx::mbar_arrive_operands(ptx::map_to_rank(ptx::smem_addr(&ctrl->ready[stage]), 0));
                 if (s0 + SLICES < slices) fetch(s0 + SLICES);
             }
         }
@@ -732,15 +795,19 @@ cudaError_t launch(const GroupedArgs& a, const Maps& maps, const Params& p, long
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// [L * E][N][R] bf16: boxes of 16 of the rank x 128 features, 32-byte swizzle
-bool map_adapters(CUtensorMap* m, const GroupedArgs& a) {
+// [L * E][N][R] bf16: boxes of `width` ranks x 128 features, swizzled over the box's rows
+bool map_adapters(CUtensorMap* m, const GroupedArgs& a, int width) {
     const EncodeTiledFn fn = tensor_map_encoder();
     if (!fn) return false;
     cuuint64_t dims[3] = {(cuuint64_t)a.R, (cuuint64_t)a.N, (cuuint64_t)a.L * a.seg.E};
     cuuint64_t strides[2] = {(cuuint64_t)a.R * 2, (cuuint64_t)a.R * a.N * 2};
-    cuuint32_t box[3] = {SLICE, BM, 1}, es[3] = {1, 1, 1};
+    cuuint32_t box[3] = {(cuuint32_t)width, BM, 1}, es[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.B), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              width == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+              : width == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                            : CU_TENSOR_MAP_SWIZZLE_32B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -775,7 +842,7 @@ cudaError_t launch_op(const GroupedArgs& a, cudaStream_t s) {
         p.lora = lora_view(a);
         p.x = static_cast<const __nv_bfloat16*>(a.rows);
         p.W = static_cast<const __nv_bfloat16*>(a.other);
-        if (!map_adapters(&m.l, a)) return cudaErrorInvalidValue;
+        if (!map_adapters(&m.l, a, p.lora.box)) return cudaErrorInvalidValue;
         if (!a.out16) return launch<kGroupedMm, false, 1, true>(a, m, p, cols, s);
         return wide(p, cols, (a.num_sms > 0 ? a.num_sms : 148) / 2) ? launch<kGroupedMm, true, 2, true>(a, m, p, cols, s)
                              : launch<kGroupedMm, true, 1, true>(a, m, p, cols, s);

@@ -28,6 +28,7 @@ constexpr int WIN = 64;                      // rows of a window
 constexpr int COLS = 64;                     // rank columns of a pass
 constexpr int KC = 64;                       // reduction per stage
 constexpr int NST = 4;
+constexpr int MAX_SPLIT = 8;                 // CTAs of a cluster, a power of two
 constexpr int TILE_BYTES = WIN * KC * 2;     // 8 KiB, either operand
 constexpr int STAGE_BYTES = 2 * TILE_BYTES;
 constexpr int PITCH = COLS + 4;              // floats of a row of partial sums
@@ -46,7 +47,7 @@ struct ShrinkParams {
 
 struct ShrinkSmem {
     SegTable seg;
-    int ids[kColumnTile];
+    alignas(16) int ids[kColumnTile];
     int list[kColumnTile];
     int warp_n[WARPS];
     int n;
@@ -74,17 +75,26 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool l
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
 // The distinct ids of ids[0, n), in order of first occurrence, into list; sm->n of them (all threads).
 __device__ __forceinline__ void distinct(ShrinkSmem* sm, int n) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    bool first = t < n && sm->ids[t] >= 0;
-    for (int j = 0; j < t && first; ++j) first = sm->ids[j] != sm->ids[t];
+    const int id = t < n ? sm->ids[t] : -1;
+    bool first = id >= 0;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(sm->ids + j);
+        first = first && !(j < t && v.x == id) && !(j + 1 < t && v.y == id) && !(j + 2 < t && v.z == id) &&
+                !(j + 3 < t && v.w == id);
+    }
     const uint32_t b = __ballot_sync(0xffffffffu, first);
     if (lane == 0) sm->warp_n[warp] = __popc(b);
     __syncthreads();
@@ -94,7 +104,7 @@ __device__ __forceinline__ void distinct(ShrinkSmem* sm, int n) {
         if (w < warp) before += sm->warp_n[w];
         total += sm->warp_n[w];
     }
-    if (first) sm->list[before + __popc(b & ((1u << lane) - 1))] = sm->ids[t];
+    if (first) sm->list[before + __popc(b & ((1u << lane) - 1))] = id;
     if (t == 0) sm->n = total;
     __syncthreads();
 }
@@ -204,15 +214,30 @@ __global__ void __launch_bounds__(THREADS) lora_shrink_kernel(const ShrinkParams
                 red[(m0 + (lane >> 2) + 8 * (j >> 1)) * PITCH + n0 + 8 * i + 2 * (lane & 3) + (j & 1)] = acc[i][j];
         ptx::cluster_sync();
         // CTA `part` finishes rows part, part + split, ...: its columns are those of the row's adapter
-        for (int o = tid; o < (WIN + p.split - 1) / p.split * COLS; o += THREADS) {
-            const int r = o / COLS * p.split + part, c = c0 + o % COLS;
+        for (int o = tid; o < WIN / p.split * (COLS / 4); o += THREADS) {
+            const int r = o / (COLS / 4) * p.split + part, q = o % (COLS / 4) * 4, c = c0 + q;
             if (r >= n || c >= ncols) continue;
-            const int a = sm.list[c / R16];
+            const int a = sm.list[c / R16];   // four neighbours belong to one adapter
             if (sm.ids[r] != a) continue;
-            float s = 0.f;
-            const uint32_t at = ptx::smem_addr(red + r * PITCH + (c - c0));
-            for (int i = 0; i < p.split; ++i) s += ld_cluster(ptx::map_to_rank(at, i));
-            p.v.u[(row0 + r) * R16 + c % R16] = __float2bfloat16_rn(c % R16 < R ? s * p.scale[a] : 0.f);
+            const uint32_t at = ptx::smem_addr(red + r * PITCH + q);
+            float4 v[MAX_SPLIT];
+#pragma unroll
+            for (int i = 0; i < MAX_SPLIT; ++i)
+                if (i < p.split) v[i] = ld_cluster4(ptx::map_to_rank(at, i));
+            float4 s = v[0];
+#pragma unroll
+            for (int i = 1; i < MAX_SPLIT; ++i)
+                if (i < p.split) {
+                    s.x += v[i].x;
+                    s.y += v[i].y;
+                    s.z += v[i].z;
+                    s.w += v[i].w;
+                }
+            const int j = c % R16;
+            const float f = p.scale[a];
+            const uint32_t lo = pack_bf16x2(j < R ? s.x * f : 0.f, j + 1 < R ? s.y * f : 0.f);
+            const uint32_t hi = pack_bf16x2(j + 2 < R ? s.z * f : 0.f, j + 3 < R ? s.w * f : 0.f);
+            *reinterpret_cast<uint2*>(p.v.u + (row0 + r) * R16 + j) = make_uint2(lo, hi);
         }
         ptx::cluster_sync();   // the ring is free again, and no CTA exits while its sums are read
     }
@@ -234,7 +259,7 @@ cudaError_t launch_lora_shrink(const GroupedArgs& a, cudaStream_t s) {
     p.windows = tiles(WIN);
     // split the reduction while the windows leave SMs idle and every part has at least four stages
     p.split = 1;
-    while (p.split < 8 && p.windows * p.split <= 2 * sms && (a.K + KC - 1) / KC >= 8 * p.split) p.split *= 2;
+    while (p.split < MAX_SPLIT && p.windows * p.split < sms && (a.K + KC - 1) / KC >= 8 * p.split) p.split *= 2;
     // passes side by side: as many as a window can have, no more than fill the SMs a few times over
     const long long most = ((long long)(a.L < WIN ? a.L : WIN) * p.v.R16 + COLS - 1) / COLS;
     const long long room = 4LL * sms / ((long long)p.windows * p.split) + 1;

@@ -6,42 +6,28 @@
 namespace moe {
 namespace ptx {
 
-// mbar_wait for a phase that threads of the other CTA of the pair arrive on:
-// their writes before the (releasing) arrive are visible afterwards.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
-    const uint32_t addr = smem_addr(bar);
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(addr), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        if (*w.abort) return false;
-        if (global_timer_ns() - t0 > w.limit_ns) {
-            record_status(w.status, MOE_ERR_TIMEOUT);
-            *w.abort = 1;
-            return false;
-        }
-    }
+// Arrive on an mbarrier of either CTA of the pair after this thread (or, behind a __syncwarp, its warp) has
+// prepared tcgen05.mma operands in its own CTA's shared memory and called fence_proxy_async.  The operands
+// are read through the asynchronous proxy, which that fence orders; an arrive with cluster-wide release would
+// also wait for every other access of the thread.
+__device__ __forceinline__ void mbar_arrive_operands(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // This thread's shared-memory writes become visible to the asynchronous proxy (tcgen05.mma operands).
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Descriptor of a K-major bf16 tile with 32-byte swizzle: rows of 32 bytes (16 bf16), 8-row groups of
-// 256 bytes (the stride byte offset); layout type 6.  The fields are those of desc_kmajor_sw128.
-__device__ __forceinline__ uint64_t desc_kmajor_sw32(uint32_t saddr) {
+// Descriptor of a K-major bf16 tile whose rows of 32, 64 or 128 bytes are swizzled over their own length:
+// 8-row groups follow each other (the stride byte offset), layout type 6, 4 or 2.  The fields are those of
+// desc_kmajor_sw128.
+__device__ __forceinline__ uint64_t desc_kmajor(uint32_t saddr, int row_bytes) {
+    const uint64_t layout = row_bytes == 128 ? 2 : row_bytes == 64 ? 4 : 6;
     uint64_t d = 0;
     d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
     d |= static_cast<uint64_t>(1) << 16;
-    d |= static_cast<uint64_t>(256 >> 4) << 32;
+    d |= static_cast<uint64_t>(8 * row_bytes >> 4) << 32;
     d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(6) << 61;
+    d |= layout << 61;
     return d;
 }
 
