@@ -145,6 +145,8 @@ inline LoraView lora_view(const GroupedArgs& a) {
 
 cudaError_t launch_grouped_simt(const GroupedArgs& a, cudaStream_t s);   // float
 cudaError_t launch_grouped_tc(const GroupedArgs& a, cudaStream_t s);     // bfloat16, M > 0
+cudaError_t launch_grouped_few(const GroupedArgs& a, cudaStream_t s);    // bfloat16 mm with few rows
+bool grouped_few(const GroupedArgs& a);                                  // whether that one is the faster
 cudaError_t launch_lora_shrink(const GroupedArgs& a, cudaStream_t s);    // u and the tiles' lists
 
 }  // namespace moe

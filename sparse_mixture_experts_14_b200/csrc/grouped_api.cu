@@ -42,6 +42,11 @@ bool on_device(GroupedArgs* a, int dev) {
     return a->status != nullptr;
 }
 
+cudaError_t launch_product(const GroupedArgs& a, cudaStream_t s) {
+    if (!a.in16) return launch_grouped_simt(a, s);
+    return a.op == kGroupedMm && grouped_few(a) ? launch_grouped_few(a, s) : launch_grouped_tc(a, s);
+}
+
 moe_status run(GroupedOp op, const void* rows, const void* other, const int32_t* offsets, const int32_t* counts,
                void* out, int M, int N, int K, int E, int dtype, int out_dtype, cudaStream_t s) {
     GroupedArgs a{};
@@ -62,7 +67,7 @@ moe_status run(GroupedOp op, const void* rows, const void* other, const int32_t*
     if (M == 0)   // no rows: every weight gradient is zero
         e = cudaMemsetAsync(out, 0, (size_t)E * N * K * (a.out16 ? 2 : 4), s);
     else
-        e = a.in16 ? launch_grouped_tc(a, s) : launch_grouped_simt(a, s);
+        e = launch_product(a, s);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -127,7 +132,7 @@ moe_status moe_grouped_lora(const void* x, const void* W, const int32_t* offsets
     const DeviceScope scope(y, false);
     if (!on_device(&a, scope.device())) return MOE_ERR_CUDA;
     if (launch_lora_shrink(a, stream) != cudaSuccess) return MOE_ERR_CUDA;
-    return launch_grouped_tc(a, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return launch_product(a, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

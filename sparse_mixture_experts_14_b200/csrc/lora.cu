@@ -120,8 +120,9 @@ __device__ __forceinline__ int adapter_of(const ShrinkParams& p, size_t r) {
 __global__ void __launch_bounds__(THREADS) lora_shrink_kernel(const ShrinkParams p) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ ShrinkSmem sm;
-    pdl_trigger();
+    // the next kernel may start once everything before this one is done: it reads all but u without waiting
     pdl_wait();
+    pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int unit = blockIdx.x / p.split, part = blockIdx.x % p.split;   // cluster, CTA of the cluster
     const bool lists = unit >= p.windows;
