@@ -42,6 +42,10 @@
 // hide an infinity or NaN in another request's adapter, so where the sum is not finite
 // the epilogue computes that output again from its own terms alone.
 //
+// Outputs of few tiles: a cluster of up to 4 pairs splits a tile's reduction (SPLIT).
+// Every pair keeps its fp32 sums in shared memory, and the CTAs add them through
+// distributed shared memory, in pair order, each storing its part of the columns.
+//
 // wgrad: the last 64-row block of a segment also holds rows of the next one, which
 // must not count, whatever they hold (NaN times zero is NaN).  The MMA stops at the
 // 16-row slice of the segment's last row, and an extra warp in each CTA clears
@@ -83,6 +87,8 @@ struct Params {
     int C;            // wgrad: columns (N)
     int red;          // mm, dgrad: length of the reduction
     int f_fast;       // wgrad: feature blocks fastest, else column blocks
+    int split;        // pairs of a cluster
+    int out16;        // split: type of the output
     void* out;
     int* status;
     long long wait_ns;
@@ -93,6 +99,7 @@ struct Params {
 };
 
 constexpr int MAX_STAGES = 6;
+constexpr int MAX_SPLIT = 4;                // pairs of a cluster
 
 struct Ctrl {
     uint64_t full[MAX_STAGES];     // leader: both CTAs' bytes of a stage landed
@@ -108,8 +115,9 @@ struct Ctrl {
     SegTable seg;
 };
 
-template <int OP, bool OUT16, int W, bool LORA>
+template <int OP, bool OUT16, int W, bool LORA, bool SPLIT>
 struct Cfg {
+    static_assert(!SPLIT || (!OUT16 && W == 1), "a split tile is summed in fp32");
     static constexpr bool WGRAD = OP == kGroupedWgrad;
     static constexpr bool A_MN = OP != kGroupedMm;
     static constexpr bool B_MN = WGRAD;
@@ -202,10 +210,10 @@ __device__ __forceinline__ float recompute(const Params& p, int e, size_t r, int
 
 __device__ __forceinline__ bool not_finite(uint32_t bits) { return (bits & 0x7f800000u) == 0x7f800000u; }
 
-template <int OP, bool OUT16, int W, bool LORA>
-__global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
+template <int OP, bool OUT16, int W, bool LORA, bool SPLIT>
+__global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
     grouped_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
-    using CF = Cfg<OP, OUT16, W, LORA>;
+    using CF = Cfg<OP, OUT16, W, LORA, SPLIT>;
     constexpr bool WGRAD = CF::WGRAD;
     constexpr int NST = CF::NST, STAGE = CF::STAGE;
     extern __shared__ uint8_t smem_raw[];
@@ -213,10 +221,13 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + NST * STAGE);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = ptx::cluster_ctarank();
+    // rank of the CTA in its pair, rank of the pair's leader in the cluster, pair of the cluster
+    const uint32_t crank = ptx::cluster_ctarank(), rank = crank & 1u, lead = crank & ~1u;
+    const int part = SPLIT ? (int)(crank >> 1) : 0, parts = SPLIT ? p.split : 1;
+    const uint16_t pair_mask = (uint16_t)(0x3u << lead);
     const bool leader = rank == 0;
-    const int cluster = blockIdx.x >> 1;
-    const int nclusters = gridDim.x >> 1;
+    const int cluster = blockIdx.x / (2 * parts);
+    const int nclusters = gridDim.x / (2 * parts);   // (split: as many as there are tiles)
 
     pdl_trigger();
     if (threadIdx.x == 0) {
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
     }
     pdl_wait();
     if (warp == 0) {
-        build_segments(&ctrl->seg, p.seg, BN, leader && cluster == 0 ? p.status : nullptr);
+        build_segments(&ctrl->seg, p.seg, BN, crank == 0 && cluster == 0 ? p.status : nullptr);
         __syncwarp();
         if (lane == 0) {
             const int nf = (p.F + CF::PAIR_F - 1) / CF::PAIR_F;
@@ -255,6 +266,10 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
 
     const uint32_t tmem_base = ctrl->tmem_base;
     const int total = ctrl->total;
+    // this pair's blocks of a tile's reduction; adapters belong to the last pair
+    auto block0 = [&](const Tile& t) { return SPLIT ? (int)((long long)t.nkb * part / parts) : 0; };
+    auto block1 = [&](const Tile& t) { return SPLIT ? (int)((long long)t.nkb * (part + 1) / parts) : t.nkb; };
+    const bool adapters_here = LORA && part == parts - 1;
     const ptx::WaitCtl wc{&ctrl->abort, p.status, (uint64_t)p.wait_ns};
 
     if (warp == 0) {
@@ -281,7 +296,8 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                     for (int i = 0; i < SLICES; ++i) z[i] = list[i / per];
                 }
                 const uint32_t bytes = W * A_BYTES + (WGRAD ? bboxes * (int)MN_LBO : (16 << box) * BK * 2);
-                for (int kb = 0; kb < t.nkb; ++kb) {
+                const int kb1 = block1(t);
+                for (int kb = block0(t); kb < kb1; ++kb) {
                     if (!ptx::mbar_wait(&ctrl->empty[stage], phase ^ 1u, wc)) {
                         aborted = true;
                         break;
@@ -302,7 +318,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                             ptx::tma_load_2d(sb + h * MN_LBO, &maps.b[0], bar, cb + h * BOX, t.row0 + k, pol);
                         tail |= 1u << stage;
                     } else {
-                        const uint32_t bar = ptx::map_to_rank(ptx::smem_addr(&ctrl->full[stage]), 0);
+                        const uint32_t bar = ptx::map_to_rank(ptx::smem_addr(&ctrl->full[stage]), lead);
                         if (leader) ptx::mbar_arrive_expect_tx(&ctrl->full[stage], 2 * bytes);
                         if (WGRAD) {
 #pragma unroll
@@ -334,7 +350,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                         phase ^= 1u;
                     }
                 }
-                if (LORA && !aborted) {
+                if (LORA && adapters_here && !aborted) {
                     for (int s0 = 0; s0 < slices; s0 += SLICES) {
                         const int n = min(SLICES, slices - s0);
                         if (!ptx::mbar_wait(&ctrl->empty[stage], phase ^ 1u, wc)) {
@@ -342,7 +358,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                             break;
                         }
                         ptx::mbar_arrive(&ctrl->land[stage]);   // the stage is free: u's warps may write it
-                        const uint32_t bar = ptx::map_to_rank(ptx::smem_addr(&ctrl->full[stage]), 0);
+                        const uint32_t bar = ptx::map_to_rank(ptx::smem_addr(&ctrl->full[stage]), lead);
                         if (leader) ptx::mbar_arrive_expect_tx(&ctrl->full[stage], 2 * n * W * SLICE_BYTES);
                         const int step = p.lora.box / SLICE;
 #pragma unroll
@@ -408,14 +424,14 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                 return ok;
             };
             auto close = [&](bool last) {
-                ptx::tc_commit_pair_multicast(&ctrl->empty[stage], 0x3);
+                ptx::tc_commit_pair_multicast(&ctrl->empty[stage], pair_mask);
                 issued = true;
                 if (++stage == NST) {
                     stage = 0;
                     phase ^= 1u;
                 }
                 if (last) {
-                    ptx::tc_commit_pair_multicast(&ctrl->tfull[acc], 0x3);
+                    ptx::tc_commit_pair_multicast(&ctrl->tfull[acc], pair_mask);
                     if (++acc == CF::ACCS) {
                         acc = 0;
                         acc_phase ^= 1u;
@@ -425,9 +441,11 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
             for (int tile = cluster; tile < total && !aborted; tile += nclusters) {
                 const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
                 const uint32_t idesc = ptx::idesc_bf16_f32(2 * BM, t.nn, CF::A_MN, CF::B_MN);
-                const int aslices = LORA ? tile_slices(p.lora, t.col_tile) : 0;
-                for (int kb = 0; kb < t.nkb; ++kb) {
-                    const bool first = OUT16 ? kb == 0 : kb % CHUNK == 0;   // of an accumulator
+                const int aslices = LORA && adapters_here ? tile_slices(p.lora, t.col_tile) : 0;
+                const int kb0 = block0(t), nkb = block1(t) - kb0;
+                for (int i = 0; i < nkb; ++i) {
+                    const int kb = kb0 + i;
+                    const bool first = OUT16 ? i == 0 : i % CHUNK == 0;   // of an accumulator
                     bool ok = open(first);
                     int slices = BK / 16;
                     if (WGRAD && kb == t.nkb - 1) {
@@ -448,12 +466,12 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                             ptx::tc_mma_bf16_pair(d_tmem + h * BN, da + h * (A_BYTES / 16) + kk * A_STEP, db + kk * B_STEP,
                                                   idesc, kk > 0 || !first);
                     }
-                    close((!OUT16 && kb % CHUNK == CHUNK - 1) || (kb == t.nkb - 1 && (!LORA || aslices == 0)));
+                    close((!OUT16 && i % CHUNK == CHUNK - 1) || (i == nkb - 1 && (!LORA || aslices == 0)));
                 }
                 if (!LORA || aborted) continue;
                 const int box = p.lora.box, step = box / SLICE;
                 const uint64_t la0 = ptx::desc_kmajor(ring, box * 2), lb0 = ptx::desc_kmajor(ring + W * A_BYTES, box * 2);
-                int kb = t.nkb;
+                int kb = nkb;
                 for (int s0 = 0; s0 < aslices; s0 += SLICES, ++kb) {
                     const bool first = !OUT16 && kb % CHUNK == 0;
                     if (!open(first) || !by_hand()) {
@@ -491,7 +509,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
             const int blk = (warp - 2) / 4 / PARTS, c0 = (warp - 2) / 4 % PARTS * CF::COLS;
             const Tile t0 = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
             const int ncol = min(CF::COLS, t0.nn - c0);   // a multiple of 32, or none (<= 0)
-            if (WGRAD && t0.nkb == 0) {
+            if (WGRAD && !SPLIT && t0.nkb == 0) {
                 // a segment without rows: nothing was accumulated, the gradient is zero
                 const int f = t0.f0 + blk * 2 * BM + (int)rank * BM + q * 32 + lane;
                 const size_t row0 = (size_t)t0.e * p.C + t0.c0 + c0;
@@ -523,7 +541,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                 ptx::tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
-                    ptx::mbar_arrive_cluster_relaxed(ptx::map_to_rank(ptx::smem_addr(&ctrl->tempty[acc]), 0));
+                    ptx::mbar_arrive_cluster_relaxed(ptx::map_to_rank(ptx::smem_addr(&ctrl->tempty[acc]), lead));
                 if (++acc == CF::ACCS) {
                     acc = 0;
                     acc_phase ^= 1u;
@@ -583,8 +601,8 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                 float sum[CF::COLS];
 #pragma unroll
                 for (int i = 0; i < CF::COLS; ++i) sum[i] = 0.f;
-                const int aslices = LORA ? tile_slices(p.lora, t0.col_tile) : 0;
-                const int nblk = t0.nkb + (aslices + SLICES - 1) / SLICES;
+                const int aslices = LORA && adapters_here ? tile_slices(p.lora, t0.col_tile) : 0;
+                const int nblk = block1(t0) - block0(t0) + (aslices + SLICES - 1) / SLICES;
                 for (int kb = 0; kb < nblk && ok; kb += CHUNK) {
                     ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->tfull[acc], acc_phase, wc));
                     if (!ok) break;
@@ -602,13 +620,21 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                     ptx::tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0)
-                        ptx::mbar_arrive_cluster_relaxed(ptx::map_to_rank(ptx::smem_addr(&ctrl->tempty[acc]), 0));
+                        ptx::mbar_arrive_cluster_relaxed(ptx::map_to_rank(ptx::smem_addr(&ctrl->tempty[acc]), lead));
                     if (++acc == CF::ACCS) {
                         acc = 0;
                         acc_phase ^= 1u;
                     }
                 }
                 if (!ok) break;
+                if (SPLIT) {
+                    // one tile per cluster: the ring is idle, every copy and MMA of this pair is done
+                    float* mine = reinterpret_cast<float*>(smem) + c0 * BM + q * 32 + lane;
+#pragma unroll
+                    for (int i = 0; i < CF::COLS; ++i)
+                        if (i < ncol) mine[i * BM] = sum[i];
+                    continue;
+                }
                 asm volatile("" : "+r"(tile));
                 const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
                 const int f = t.f0 + blk * 2 * BM + (int)rank * BM + q * 32 + lane;
@@ -645,8 +671,8 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
         uint32_t land_phase = 0;   // per stage
         for (int tile = cluster; tile < total; tile += nclusters) {
             const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
-            block += t.nkb;
-            if ((t.rows & 15) == 0) continue;
+            block += block1(t) - block0(t);
+            if ((t.rows & 15) == 0 || block1(t) != t.nkb) continue;
             const int stage = (block - 1) % NST;
             bool ok = ptx::mbar_wait(&ctrl->land[stage], land_phase >> stage & 1, wc);
             ok = __all_sync(0xffffffffu, ok);
@@ -662,7 +688,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
             }
             ptx::fence_proxy_async();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_operands(ptx::map_to_rank(ptx::smem_addr(&ctrl->ready[stage]), 0));
+            if (lane == 0) ptx::mbar_arrive_operands(ptx::map_to_rank(ptx::smem_addr(&ctrl->ready[stage]), lead));
         }
     } else if (LORA) {
         // ---------------------------------------------------------------- rows of u (both CTAs)
@@ -676,7 +702,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
         const int t0 = (warp - 2 - CF::EPI_WARPS) * 32 + lane;   // this thread's rows of the half: t0, t0 + 64
         for (int tile = cluster; tile < total && ok; tile += nclusters) {
             const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
-            const int slices = tile_slices(p.lora, t.col_tile);
+            const int slices = adapters_here ? tile_slices(p.lora, t.col_tile) : 0;
             const int32_t* list = p.lora.tile_list + (size_t)t.col_tile * BN;
             const int32_t head = lane < slices / per ? list[lane] : -1;   // the list's first 32 adapters
             int id[2];
@@ -708,7 +734,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                 }
             };
             if (slices > 0) fetch(0);
-            block += t.nkb;
+            block += block1(t) - block0(t);
             for (int s0 = 0; s0 < slices; s0 += SLICES, ++block) {
                 const int stage = block % NST;
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->land[stage], land_phase >> stage & 1, wc));
@@ -731,12 +757,52 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA>::THREADS, 1)
                 }
                 ptx::fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_operands(ptx::map_to_rank(ptx::smem_addr(&ctrl->ready[stage]), 0));
+                if (lane == 0) ptx::mbar_arrive_operands(ptx::map_to_rank(ptx::smem_addr(&ctrl->ready[stage]), lead));
                 if (s0 + SLICES < slices) fetch(s0 + SLICES);
             }
         }
     }
 
+    if (SPLIT) {
+        ptx::tc_fence_before_sync();
+        __syncwarp();
+        ptx::cluster_sync();
+        if (cluster < total) {
+            // the columns of this CTA's features: part, part + parts, ... in turn, a warp a column, four
+            // features a lane
+            const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, cluster);
+            const size_t row0 = (WGRAD ? (size_t)t.e * p.C : (size_t)0) + t.c0;
+            const int f = t.f0 + (int)rank * BM + 4 * lane;
+            const uint32_t mine = ptx::smem_addr(smem) + 16 * lane;
+            for (int c = part + parts * warp; c < t.valid; c += parts * (CF::THREADS / 32)) {
+                float4 v[MAX_SPLIT];
+#pragma unroll
+                for (int i = 0; i < MAX_SPLIT; ++i)
+                    if (i < parts) v[i] = ptx::ld_cluster4(ptx::map_to_rank(mine + c * BM * 4, 2 * i + rank));
+                float s[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+                for (int i = 1; i < MAX_SPLIT; ++i)
+                    if (i < parts) {
+                        s[0] += v[i].x;
+                        s[1] += v[i].y;
+                        s[2] += v[i].z;
+                        s[3] += v[i].w;
+                    }
+                if (f >= p.F) continue;   // F is a multiple of 8
+                if (LORA) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (not_finite(__float_as_uint(s[j]))) s[j] = recompute(p, t.e, row0 + c, f + j);
+                }
+                if (p.out16)
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + (row0 + c) * p.F + f) =
+                        make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+                else
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + (row0 + c) * p.F + f) =
+                        make_float4(s[0], s[1], s[2], s[3]);
+            }
+        }
+    }
     ptx::tc_fence_before_sync();
     __syncwarp();
     ptx::cluster_sync();
@@ -755,19 +821,19 @@ bool wide(const Params& p, long long cols, int pairs) {
     return cols * nf >= 2LL * pairs && nf * 512 * 8 <= (long long)p.F * 9;
 }
 
-template <int OP, bool OUT16, int W, bool LORA = false>
+template <int OP, bool OUT16, int W, bool LORA = false, bool SPLIT = false>
 cudaError_t launch(const GroupedArgs& a, const Maps& maps, const Params& p, long long col_tiles, cudaStream_t s) {
-    using CF = Cfg<OP, OUT16, W, LORA>;
+    using CF = Cfg<OP, OUT16, W, LORA, SPLIT>;
     static PerDeviceOnce attr;
     cudaError_t e = attr.run([] {
-        return cudaFuncSetAttribute(grouped_tc_kernel<OP, OUT16, W, LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(grouped_tc_kernel<OP, OUT16, W, LORA, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     CF::SMEM);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.x = SPLIT ? 2 * p.split : 2;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -776,23 +842,40 @@ cudaError_t launch(const GroupedArgs& a, const Maps& maps, const Params& p, long
     cfg.dynamicSmemBytes = CF::SMEM;
     cfg.stream = s;
     cfg.attrs = at;
-    static PerDeviceInt clusters;
-    const int most = clusters.get([&] {
-        cudaLaunchConfig_t q = cfg;
-        q.gridDim = dim3(2 * 74);
-        q.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, grouped_tc_kernel<OP, OUT16, W, LORA>, &q) != cudaSuccess || n <= 0) {
-            cudaGetLastError();
-            n = (a.num_sms > 0 ? a.num_sms : 148) / 2;
-        }
-        return n;
-    });
+    const int most = SPLIT ? 0 : [&] {
+        static PerDeviceInt clusters;
+        return clusters.get([&] {
+            cudaLaunchConfig_t q = cfg;
+            q.gridDim = dim3(2 * 74);
+            q.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, grouped_tc_kernel<OP, OUT16, W, LORA, SPLIT>, &q) != cudaSuccess ||
+                n <= 0) {
+                cudaGetLastError();
+                n = (a.num_sms > 0 ? a.num_sms : 148) / 2;
+            }
+            return n;
+        });
+    }();
+
     const long long tiles = col_tiles * ((p.F + CF::PAIR_F - 1) / CF::PAIR_F);
-    cfg.gridDim = dim3((unsigned)(2 * (tiles < most ? (tiles > 0 ? tiles : 1) : most)));
+    const long long pairs = SPLIT ? tiles * p.split : tiles < most ? tiles : most;
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, grouped_tc_kernel<OP, OUT16, W, LORA>, maps, p);
+    e = cudaLaunchKernelEx(&cfg, grouped_tc_kernel<OP, OUT16, W, LORA, SPLIT>, maps, p);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Pairs that split a tile's reduction: while twice as many still fit on the SMs at once, and each keeps at
+// least four blocks.
+int split_of(const Params& p, const GroupedArgs& a, long long cols) {
+    const long long tiles = cols * ((p.F + 2 * BM - 1) / (2 * BM));
+    const int sms = a.num_sms > 0 ? a.num_sms : 148;
+    // wgrad: the reduction is the segments' rows, on average
+    const int blocks = (a.op == kGroupedWgrad ? a.seg.M / a.seg.E : p.red) / BK;
+    int s = 1;
+    while (s < MAX_SPLIT && 2 * tiles * s <= 64LL * sms / 148 && blocks >= 8 * s) s *= 2;
+    return s;
 }
 
 // [L * E][N][R] bf16: boxes of `width` ranks x 128 features, swizzled over the box's rows
@@ -838,16 +921,20 @@ cudaError_t launch_op(const GroupedArgs& a, cudaStream_t s) {
         if (cols > M) cols = M;   // a segment with rows has at least one
     }
     if (!ok) return cudaErrorInvalidValue;
+    p.out16 = a.out16;
+    p.split = split_of(p, a, cols);
     if (OP == kGroupedMm && a.A) {
         p.lora = lora_view(a);
         p.x = static_cast<const __nv_bfloat16*>(a.rows);
         p.W = static_cast<const __nv_bfloat16*>(a.other);
         if (!map_adapters(&m.l, a, p.lora.box)) return cudaErrorInvalidValue;
+        if (p.split > 1) return launch<kGroupedMm, false, 1, true, true>(a, m, p, cols, s);
         if (!a.out16) return launch<kGroupedMm, false, 1, true>(a, m, p, cols, s);
         return wide(p, cols, (a.num_sms > 0 ? a.num_sms : 148) / 2) ? launch<kGroupedMm, true, 2, true>(a, m, p, cols, s)
                              : launch<kGroupedMm, true, 1, true>(a, m, p, cols, s);
     }
     m.l = m.a;
+    if (p.split > 1) return launch<OP, false, 1, false, true>(a, m, p, cols, s);
     if (!a.out16) return launch<OP, false, 1>(a, m, p, cols, s);
     return wide(p, cols, (a.num_sms > 0 ? a.num_sms : 148) / 2) ? launch<OP, true, 2>(a, m, p, cols, s) : launch<OP, true, 1>(a, m, p, cols, s);
 }

@@ -75,15 +75,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool l
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
 // The distinct ids of ids[0, n), in order of first occurrence, into list; sm->n of them (all threads).
 __device__ __forceinline__ void distinct(ShrinkSmem* sm, int n) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -224,7 +215,7 @@ __global__ void __launch_bounds__(THREADS) lora_shrink_kernel(const ShrinkParams
             float4 v[MAX_SPLIT];
 #pragma unroll
             for (int i = 0; i < MAX_SPLIT; ++i)
-                if (i < p.split) v[i] = ld_cluster4(ptx::map_to_rank(at, i));
+                if (i < p.split) v[i] = ptx::ld_cluster4(ptx::map_to_rank(at, i));
             float4 s = v[0];
 #pragma unroll
             for (int i = 1; i < MAX_SPLIT; ++i)

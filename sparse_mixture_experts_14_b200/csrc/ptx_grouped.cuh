@@ -31,5 +31,15 @@ __device__ __forceinline__ uint64_t desc_kmajor(uint32_t saddr, int row_bytes) {
     return d;
 }
 
+// 16 bytes of a cluster's shared memory.
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 }  // namespace ptx
 }  // namespace moe
