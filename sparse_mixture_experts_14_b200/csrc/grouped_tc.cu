@@ -266,10 +266,18 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
 
     const uint32_t tmem_base = ctrl->tmem_base;
     const int total = ctrl->total;
-    // this pair's blocks of a tile's reduction; adapters belong to the last pair
-    auto block0 = [&](const Tile& t) { return SPLIT ? (int)((long long)t.nkb * part / parts) : 0; };
-    auto block1 = [&](const Tile& t) { return SPLIT ? (int)((long long)t.nkb * (part + 1) / parts) : t.nkb; };
-    const bool adapters_here = LORA && part == parts - 1;
+    // this pair's share of a tile: blocks [kb0, kb1) of the reduction, slices [s0, s1) of the adapters
+    struct Share {
+        int kb0, kb1, s0, s1;
+    };
+    auto share = [&](const Tile& t) {
+        const int slices = LORA ? tile_slices(p.lora, t.col_tile) : 0;
+        if (!SPLIT) return Share{0, t.nkb, 0, slices};
+        const long long all = t.nkb + (slices + SLICES - 1) / SLICES;
+        const int b0 = (int)(all * part / parts), b1 = (int)(all * (part + 1) / parts);
+        return Share{min(b0, t.nkb), min(b1, t.nkb), max(b0 - t.nkb, 0) * SLICES,
+                     min(max(b1 - t.nkb, 0) * SLICES, slices)};
+    };
     const ptx::WaitCtl wc{&ctrl->abort, p.status, (uint64_t)p.wait_ns};
 
     if (warp == 0) {
@@ -289,15 +297,15 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                 const int bboxes = WGRAD ? (half + BOX - 1) / BOX : 1;
                 // (asked for now, needed behind the last of the other blocks)
                 const int32_t* list = LORA ? p.lora.tile_list + (size_t)t.col_tile * BN : nullptr;
-                const int slices = LORA ? tile_slices(p.lora, t.col_tile) : 0, per = LORA ? p.lora.R16 / SLICE : 1;
+                const int per = LORA ? p.lora.R16 / SLICE : 1;
+                const Share sh = share(t);
                 int z[SLICES];
                 if (LORA) {
 #pragma unroll
-                    for (int i = 0; i < SLICES; ++i) z[i] = list[i / per];
+                    for (int i = 0; i < SLICES; ++i) z[i] = list[(sh.s0 + i) / per];
                 }
                 const uint32_t bytes = W * A_BYTES + (WGRAD ? bboxes * (int)MN_LBO : (16 << box) * BK * 2);
-                const int kb1 = block1(t);
-                for (int kb = block0(t); kb < kb1; ++kb) {
+                for (int kb = sh.kb0; kb < sh.kb1; ++kb) {
                     if (!ptx::mbar_wait(&ctrl->empty[stage], phase ^ 1u, wc)) {
                         aborted = true;
                         break;
@@ -350,9 +358,9 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                         phase ^= 1u;
                     }
                 }
-                if (LORA && adapters_here && !aborted) {
-                    for (int s0 = 0; s0 < slices; s0 += SLICES) {
-                        const int n = min(SLICES, slices - s0);
+                if (LORA && !aborted) {
+                    for (int s0 = sh.s0; s0 < sh.s1; s0 += SLICES) {
+                        const int n = min(SLICES, sh.s1 - s0);
                         if (!ptx::mbar_wait(&ctrl->empty[stage], phase ^ 1u, wc)) {
                             aborted = true;
                             break;
@@ -372,7 +380,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                                                       pol);
                         }
 #pragma unroll
-                        for (int i = 0; i < SLICES; ++i) z[i] = list[min(s0 + SLICES + i, slices - 1) / per];
+                        for (int i = 0; i < SLICES; ++i) z[i] = list[min(s0 + SLICES + i, sh.s1 - 1) / per];
                         armed |= 1u << stage;
                         armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
                         if (++stage == NST) {
@@ -441,8 +449,8 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
             for (int tile = cluster; tile < total && !aborted; tile += nclusters) {
                 const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
                 const uint32_t idesc = ptx::idesc_bf16_f32(2 * BM, t.nn, CF::A_MN, CF::B_MN);
-                const int aslices = LORA && adapters_here ? tile_slices(p.lora, t.col_tile) : 0;
-                const int kb0 = block0(t), nkb = block1(t) - kb0;
+                const Share sh = share(t);
+                const int kb0 = sh.kb0, nkb = sh.kb1 - kb0, aslices = sh.s1 - sh.s0;
                 for (int i = 0; i < nkb; ++i) {
                     const int kb = kb0 + i;
                     const bool first = OUT16 ? i == 0 : i % CHUNK == 0;   // of an accumulator
@@ -601,8 +609,9 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                 float sum[CF::COLS];
 #pragma unroll
                 for (int i = 0; i < CF::COLS; ++i) sum[i] = 0.f;
-                const int aslices = LORA && adapters_here ? tile_slices(p.lora, t0.col_tile) : 0;
-                const int nblk = block1(t0) - block0(t0) + (aslices + SLICES - 1) / SLICES;
+                const Share sh = share(t0);
+                const int aslices = sh.s1 - sh.s0;
+                const int nblk = sh.kb1 - sh.kb0 + (aslices + SLICES - 1) / SLICES;
                 for (int kb = 0; kb < nblk && ok; kb += CHUNK) {
                     ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->tfull[acc], acc_phase, wc));
                     if (!ok) break;
@@ -671,8 +680,9 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
         uint32_t land_phase = 0;   // per stage
         for (int tile = cluster; tile < total; tile += nclusters) {
             const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
-            block += block1(t) - block0(t);
-            if ((t.rows & 15) == 0 || block1(t) != t.nkb) continue;
+            const Share sh = share(t);
+            block += sh.kb1 - sh.kb0;
+            if ((t.rows & 15) == 0 || sh.kb1 != t.nkb || sh.kb0 == sh.kb1) continue;
             const int stage = (block - 1) % NST;
             bool ok = ptx::mbar_wait(&ctrl->land[stage], land_phase >> stage & 1, wc);
             ok = __all_sync(0xffffffffu, ok);
@@ -702,9 +712,10 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
         const int t0 = (warp - 2 - CF::EPI_WARPS) * 32 + lane;   // this thread's rows of the half: t0, t0 + 64
         for (int tile = cluster; tile < total && ok; tile += nclusters) {
             const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
-            const int slices = adapters_here ? tile_slices(p.lora, t.col_tile) : 0;
+            const Share sh = share(t);
+            const int slices = sh.s1;
             const int32_t* list = p.lora.tile_list + (size_t)t.col_tile * BN;
-            const int32_t head = lane < slices / per ? list[lane] : -1;   // the list's first 32 adapters
+            const int32_t head = lane * per < slices ? list[lane] : -1;   // the list's first 32 adapters
             int id[2];
             const uint4* u[2];
 #pragma unroll
@@ -733,9 +744,9 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                     }
                 }
             };
-            if (slices > 0) fetch(0);
-            block += block1(t) - block0(t);
-            for (int s0 = 0; s0 < slices; s0 += SLICES, ++block) {
+            if (sh.s0 < slices) fetch(sh.s0);
+            block += sh.kb1 - sh.kb0;
+            for (int s0 = sh.s0; s0 < slices; s0 += SLICES, ++block) {
                 const int stage = block % NST;
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->land[stage], land_phase >> stage & 1, wc));
                 if (!ok) break;
@@ -866,15 +877,43 @@ cudaError_t launch(const GroupedArgs& a, const Maps& maps, const Params& p, long
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Pairs that split a tile's reduction: while twice as many still fit on the SMs at once, and each keeps at
-// least four blocks.
+// Clusters of 2 * split CTAs that run at once (a cluster stays within a GPC, so large ones leave SMs over).
+template <int OP, bool LORA>
+int split_clusters(int split) {
+    using CF = Cfg<OP, false, 1, LORA, true>;
+    static PerDeviceInt known[MAX_SPLIT + 1];
+    return known[split].get([&] {
+        cudaLaunchConfig_t q = {};
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2 * split;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        q.gridDim = dim3(2 * 72);
+        q.blockDim = dim3(CF::THREADS);
+        q.dynamicSmemBytes = CF::SMEM;
+        q.attrs = at;
+        q.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(grouped_tc_kernel<OP, false, 1, LORA, true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, CF::SMEM) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, grouped_tc_kernel<OP, false, 1, LORA, true>, &q) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        return n;
+    });
+}
+
+// Pairs that split a tile's reduction: as many as run at once and keep at least four blocks each.
+template <int OP, bool LORA>
 int split_of(const Params& p, const GroupedArgs& a, long long cols) {
     const long long tiles = cols * ((p.F + 2 * BM - 1) / (2 * BM));
-    const int sms = a.num_sms > 0 ? a.num_sms : 148;
     // wgrad: the reduction is the segments' rows, on average
-    const int blocks = (a.op == kGroupedWgrad ? a.seg.M / a.seg.E : p.red) / BK;
+    const int blocks = (OP == kGroupedWgrad ? a.seg.M / a.seg.E : p.red) / BK;
     int s = 1;
-    while (s < MAX_SPLIT && 2 * tiles * s <= 64LL * sms / 148 && blocks >= 8 * s) s *= 2;
+    for (int t = 2; t <= MAX_SPLIT; ++t)
+        if (blocks >= 4 * t && tiles <= split_clusters<OP, LORA>(t)) s = t;
     return s;
 }
 
@@ -922,8 +961,8 @@ cudaError_t launch_op(const GroupedArgs& a, cudaStream_t s) {
     }
     if (!ok) return cudaErrorInvalidValue;
     p.out16 = a.out16;
-    p.split = split_of(p, a, cols);
     if (OP == kGroupedMm && a.A) {
+        p.split = split_of<kGroupedMm, true>(p, a, cols);
         p.lora = lora_view(a);
         p.x = static_cast<const __nv_bfloat16*>(a.rows);
         p.W = static_cast<const __nv_bfloat16*>(a.other);
@@ -934,6 +973,7 @@ cudaError_t launch_op(const GroupedArgs& a, cudaStream_t s) {
                              : launch<kGroupedMm, true, 1, true>(a, m, p, cols, s);
     }
     m.l = m.a;
+    p.split = split_of<OP, false>(p, a, cols);
     if (p.split > 1) return launch<OP, false, 1, false, true>(a, m, p, cols, s);
     if (!a.out16) return launch<OP, false, 1>(a, m, p, cols, s);
     return wide(p, cols, (a.num_sms > 0 ? a.num_sms : 148) / 2) ? launch<OP, true, 2>(a, m, p, cols, s) : launch<OP, true, 1>(a, m, p, cols, s);
