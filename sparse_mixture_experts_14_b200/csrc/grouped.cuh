@@ -112,20 +112,24 @@ __host__ __device__ inline int column_tile_height(int n) {
     return tt > 0 ? ((n + tt - 1) / tt + 31) / 32 * 32 : 32;
 }
 
-// The adapters as the products' kernels see them.  u is a workspace buffer [M][R16], R16 = R rounded
-// up to 16 (zeros behind R); rows without an adapter hold nothing.
+// The adapters as the products' kernels see them.  u is a workspace buffer [M][terms][R16], R16 = R
+// rounded up to 16 (zeros behind R); rows without an adapter hold nothing.  For a bf16 output u is one bf16
+// value, rounded like the operand it becomes; beside an fp32 output that rounding (2^-9 of u) would be the
+// largest error by far, so there u is the sum of three bf16 values, which hold fp32's 24 bits.
 struct LoraView {
     const __nv_bfloat16* B;        // [L][E][N][R]
     const int32_t* adapter;        // [M]
-    __nv_bfloat16* u;              // [M][R16]
+    __nv_bfloat16* u;              // [M][terms][R16]
     int32_t* tile_list;            // [column tiles][256]: the adapters that occur in the tile, each once
     int32_t* tile_count;           // [column tiles]
     int L, R, R16;
+    int terms;                     // 1 or 3
+    int per;                       // 16-wide slices of an adapter's part of a row of u
     int box;                       // ranks of a box of B: the widest of 64, 32, 16 that divides R16
 };
 
 inline size_t lora_tiles(int M, int E) { return (size_t)M / kColumnTile + E; }
-inline size_t lora_u_bytes(int M, int R) { return align_up((size_t)M * ((R + 15) / 16 * 16) * 2, 256); }
+inline size_t lora_u_bytes(int M, int R) { return align_up((size_t)M * 3 * ((R + 15) / 16 * 16) * 2, 256); }
 inline size_t lora_workspace_bytes(int M, int E, int R) {
     return lora_u_bytes(M, R) + align_up(lora_tiles(M, E) * (kColumnTile + 1) * 4, 256);
 }
@@ -139,6 +143,8 @@ inline LoraView lora_view(const GroupedArgs& a) {
     v.L = a.L;
     v.R = a.R;
     v.R16 = (a.R + 15) / 16 * 16;
+    v.terms = a.out16 ? 1 : 3;
+    v.per = v.terms * v.R16 / 16;
     v.box = v.R16 % 64 == 0 ? 64 : v.R16 % 32 == 0 ? 32 : 16;
     return v;
 }

@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT <= 2 ? 2 : 1) grouped_few_kerne
     constexpr int ROWS = 8 * NT;
     constexpr int U = NT <= 2 ? 4 : 2;     // steps whose loads are in flight together
     constexpr int PITCH = FEATURES + 1;
+    constexpr int TERMS = OUT16 ? 1 : 3;
     __shared__ SegTable seg;
     __shared__ float red[WARPS][ROWS][PITCH];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -118,15 +119,30 @@ __global__ void __launch_bounds__(32 * WARPS, NT <= 2 ? 2 : 1) grouped_few_kerne
             for (int t = 0; t < NT; ++t)
                 b[u][t] = in && xl[t] ? __ldg(reinterpret_cast<const uint4*>(x[t] + k)) : zero;
         }
+        // fp32 outputs: the tensor cores truncate as they accumulate, so they take a few steps at a time and
+        // the sums go on with rounding (a reduction of 14336: error 1.8e-6 -> 1.5e-7 of the result)
+        float part[MT][NT][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) part[i][t][c] = OUT16 ? acc[i][t][c] : 0.f;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    mma16816(acc[i][t], a[u][i][0].x, a[u][i][1].x, a[u][i][0].y, a[u][i][1].y, b[u][t].x, b[u][t].y);
-                    mma16816(acc[i][t], a[u][i][0].z, a[u][i][1].z, a[u][i][0].w, a[u][i][1].w, b[u][t].z, b[u][t].w);
+                    mma16816(part[i][t], a[u][i][0].x, a[u][i][1].x, a[u][i][0].y, a[u][i][1].y, b[u][t].x, b[u][t].y);
+                    mma16816(part[i][t], a[u][i][0].z, a[u][i][1].z, a[u][i][0].w, a[u][i][1].w, b[u][t].z, b[u][t].w);
                 }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[i][t][c] = OUT16 ? part[i][t][c] : acc[i][t][c] + part[i][t][c];
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -148,19 +164,27 @@ __global__ void __launch_bounds__(32 * WARPS, NT <= 2 ? 2 : 1) grouped_few_kerne
             if (id >= 0 && id < p.lora.L) {
                 const uint4* bl = reinterpret_cast<const uint4*>(
                     p.lora.B + (((size_t)id * p.seg.E + e) * N + f) * p.lora.R);
-                const uint4* ul = reinterpret_cast<const uint4*>(p.lora.u + (row0 + r) * p.lora.R16);
+                const uint4* ul = reinterpret_cast<const uint4*>(p.lora.u + (row0 + r) * TERMS * p.lora.R16);
                 float d = 0.f;
 #pragma unroll 2
                 for (int j = 0; j < p.lora.R / 8; ++j) {
-                    const uint4 m = __ldg(bl + j), n = ul[j];
-                    d = fmaf(bf16_lo(m.x), bf16_lo(n.x), d);
-                    d = fmaf(bf16_hi(m.x), bf16_hi(n.x), d);
-                    d = fmaf(bf16_lo(m.y), bf16_lo(n.y), d);
-                    d = fmaf(bf16_hi(m.y), bf16_hi(n.y), d);
-                    d = fmaf(bf16_lo(m.z), bf16_lo(n.z), d);
-                    d = fmaf(bf16_hi(m.z), bf16_hi(n.z), d);
-                    d = fmaf(bf16_lo(m.w), bf16_lo(n.w), d);
-                    d = fmaf(bf16_hi(m.w), bf16_hi(n.w), d);
+                    const uint4 m = __ldg(bl + j);
+                    const uint32_t mw[4] = {m.x, m.y, m.z, m.w};
+                    uint4 n[TERMS];
+#pragma unroll
+                    for (int t = 0; t < TERMS; ++t) n[t] = ul[t * (p.lora.R16 / 8) + j];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float lo = 0.f, hi = 0.f;
+#pragma unroll
+                        for (int t = TERMS - 1; t >= 0; --t) {   // (exact)
+                            const uint32_t nw = i == 0 ? n[t].x : i == 1 ? n[t].y : i == 2 ? n[t].z : n[t].w;
+                            lo += bf16_lo(nw);
+                            hi += bf16_hi(nw);
+                        }
+                        d = fmaf(bf16_lo(mw[i]), lo, d);
+                        d = fmaf(bf16_hi(mw[i]), hi, d);
+                    }
                 }
                 s += d;
             }

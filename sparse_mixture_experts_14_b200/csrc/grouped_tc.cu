@@ -37,8 +37,7 @@
 // of its rank, the ring takes boxes of B_{a,e} (A side) and, written by two extra warps,
 // the tile's rows of u with zeros in the rows of other adapters (B side): one K = 16
 // MMA a slice, four slices a stage.  Boxes are 64, 32 or 16 ranks wide, the widest
-// that divides the padded rank, with the swizzle of that width: TMA's time goes by
-// rows (rank 64 in boxes of 16 cost a prefill 71 us of 413, in boxes of 64 BOXUS).  A zero does not
+// that divides the padded rank, with the swizzle of that width.  A zero does not
 // hide an infinity or NaN in another request's adapter, so where the sum is not finite
 // the epilogue computes that output again from its own terms alone.
 //
@@ -179,9 +178,9 @@ __device__ __forceinline__ Tile decode(const Ctrl* c, const Params& p, int tile)
 // Index of the row box that holds n rows (n a multiple of 16, at most 128).
 __device__ __forceinline__ int box_of(int n) { return n <= 16 ? 0 : n <= 32 ? 1 : n <= 64 ? 2 : 3; }
 
-// Adapter slices of a tile: (adapters among its rows) x (slices of the rank).
+// Adapter slices of a tile: (adapters among its rows) x (slices of u's row).
 __device__ __forceinline__ int tile_slices(const LoraView& l, int col_tile) {
-    return l.tile_count[col_tile] * (l.R16 / SLICE);
+    return l.tile_count[col_tile] * l.per;
 }
 
 // What the TMA's swizzle of rows of 2 box bytes does to row r: its 16-byte chunk c is kept at c ^ swizzle.
@@ -200,10 +199,14 @@ __device__ __forceinline__ float recompute(const Params& p, int e, size_t r, int
     }
     const int id = p.lora.adapter[r];
     if (id >= 0 && id < p.lora.L) {
-        const __nv_bfloat16* u = p.lora.u + r * p.lora.R16;
+        const __nv_bfloat16* u = p.lora.u + r * p.lora.terms * p.lora.R16;
         const __nv_bfloat16* b = p.lora.B + (((size_t)id * p.seg.E + e) * p.F + f) * p.lora.R;
 #pragma unroll 1
-        for (int j = 0; j < p.lora.R; ++j) s = fmaf(__bfloat162float(u[j]), __bfloat162float(b[j]), s);
+        for (int j = 0; j < p.lora.R; ++j) {
+            float v = 0.f;
+            for (int t = p.lora.terms - 1; t >= 0; --t) v += __bfloat162float(u[t * p.lora.R16 + j]);
+            s = fmaf(v, __bfloat162float(b[j]), s);
+        }
     }
     return s;
 }
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                 const int bboxes = WGRAD ? (half + BOX - 1) / BOX : 1;
                 // (asked for now, needed behind the last of the other blocks)
                 const int32_t* list = LORA ? p.lora.tile_list + (size_t)t.col_tile * BN : nullptr;
-                const int per = LORA ? p.lora.R16 / SLICE : 1;
+                const int per = LORA ? p.lora.per : 1;
                 const Share sh = share(t);
                 int z[SLICES];
                 if (LORA) {
@@ -376,7 +379,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
 #pragma unroll
                             for (int h = 0; h < W; ++h)
                                 ptx::tma_load_3d_pair(smem + stage * STAGE + h * A_BYTES + i * SLICE_BYTES, &maps.l, bar,
-                                                      (s0 + i) % per * SLICE, fa + h * 2 * BM, z[i] * p.seg.E + t.e,
+                                                      (s0 + i) % per % (p.lora.R16 / SLICE) * SLICE, fa + h * 2 * BM, z[i] * p.seg.E + t.e,
                                                       pol);
                         }
 #pragma unroll
@@ -708,7 +711,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
         unsigned block = 0;        // blocks through the ring so far
         uint32_t land_phase = 0;   // per stage
         bool ok = true;
-        const int per = p.lora.R16 / SLICE, box = p.lora.box, step = box / SLICE;
+        const int per = p.lora.per, box = p.lora.box, step = box / SLICE;
         const int t0 = (warp - 2 - CF::EPI_WARPS) * 32 + lane;   // this thread's rows of the half: t0, t0 + 64
         for (int tile = cluster; tile < total && ok; tile += nclusters) {
             const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
@@ -723,7 +726,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                 const int r = t0 + 64 * j, col = (int)rank * (t.nn / 2) + r;
                 const bool live = r < t.nn / 2 && col < t.valid;
                 id[j] = live ? p.lora.adapter[(size_t)t.c0 + col] : -1;
-                u[j] = reinterpret_cast<const uint4*>(p.lora.u + ((size_t)t.c0 + (live ? col : 0)) * p.lora.R16);
+                u[j] = reinterpret_cast<const uint4*>(p.lora.u + ((size_t)t.c0 + (live ? col : 0)) * p.lora.terms * p.lora.R16);
             }
             // the rows' part of four slices: read ahead of the wait for the stage
             uint4 v[SLICES][2][2];

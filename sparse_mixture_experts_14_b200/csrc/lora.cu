@@ -1,7 +1,8 @@
 // Low-rank adapters beside a grouped product, first half: u_r = s_a A_{a,e} x_r for
 // every row r of expert e's segment with adapter a = adapter[r] (-1: none, the row
-// takes no part), rounded once to bf16, the operand type of the second half
-// y_r = W_e x_r + B_{a,e} u_r (grouped_tc.cu).
+// takes no part), as the bf16 operand of the second half y_r = W_e x_r + B_{a,e} u_r
+// (grouped_tc.cu, grouped_few.cu): one bf16 value, or three that add up to the fp32
+// one where the output is fp32.
 //
 // A cluster takes a window of 64 rows of a segment, finds the adapters that occur in
 // it, and multiplies the window with 64 rank columns at a time (a column: one rank of
@@ -227,9 +228,17 @@ __global__ void __launch_bounds__(THREADS) lora_shrink_kernel(const ShrinkParams
                 }
             const int j = c % R16;
             const float f = p.scale[a];
-            const uint32_t lo = pack_bf16x2(j < R ? s.x * f : 0.f, j + 1 < R ? s.y * f : 0.f);
-            const uint32_t hi = pack_bf16x2(j + 2 < R ? s.z * f : 0.f, j + 3 < R ? s.w * f : 0.f);
-            *reinterpret_cast<uint2*>(p.v.u + (row0 + r) * R16 + j) = make_uint2(lo, hi);
+            float y[4] = {j < R ? s.x * f : 0.f, j + 1 < R ? s.y * f : 0.f, j + 2 < R ? s.z * f : 0.f,
+                          j + 3 < R ? s.w * f : 0.f};
+            __nv_bfloat16* u = p.v.u + (row0 + r) * p.v.terms * R16 + j;
+            for (int t = 0; t < p.v.terms; ++t) {
+                const uint32_t lo = pack_bf16x2(y[0], y[1]), hi = pack_bf16x2(y[2], y[3]);
+                *reinterpret_cast<uint2*>(u + t * R16) = make_uint2(lo, hi);
+                // what the term leaves over (exact); nothing where it is not finite
+                const float z[4] = {bf16_lo(lo), bf16_hi(lo), bf16_lo(hi), bf16_hi(hi)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = isfinite(z[i]) ? y[i] - z[i] : 0.f;
+            }
         }
         ptx::cluster_sync();   // the ring is free again, and no CTA exits while its sums are read
     }

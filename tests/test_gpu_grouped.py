@@ -98,18 +98,19 @@ def test_odd_sizes(moe, op, types, size, seg):
 
 @pytest.mark.parametrize("op", ["mm", "dgrad", "wgrad"])
 @pytest.mark.parametrize("counts", [[1500, 0, 2600, 900], [9, 8, 0, 7], [60, 200, 2, 90]], ids=str)
-def test_larger(moe, op, counts):
-    """Several waves of tiles, long reductions."""
-    N, K = 2056, 1736
+@pytest.mark.parametrize("N,K", [(2056, 1736), (5120, 640), (1024, 4608)], ids=str)
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+def test_larger(moe, op, counts, N, K, out_dtype):
+    """Several waves of tiles, narrow and wide (512 features), few tiles with long reductions."""
     starts, rows = segments(counts)
     off, cnt = device_segments(counts, starts, rows, False)
     gen = torch.Generator(device="cuda").manual_seed(13)
     x, dy = randn(gen, (rows, K), 1.0, DT["bf16"]), randn(gen, (rows, N), 0.5, DT["bf16"])
     W = randn(gen, (len(counts), N, K), K ** -0.5, DT["bf16"])
-    out = _run(moe, op, x, dy, W, off, cnt, _out(op, rows, len(counts), N, K, "bf16"))
+    out = _run(moe, op, x, dy, W, off, cnt, _out(op, rows, len(counts), N, K, out_dtype))
     assert moe.moe_get_device_status() == moe.MOE_OK
     _verify(op, out, counts, starts, x, dy, W)
-    again = _run(moe, op, x, dy, W, off, cnt, _out(op, rows, len(counts), N, K, "bf16"))
+    again = _run(moe, op, x, dy, W, off, cnt, _out(op, rows, len(counts), N, K, out_dtype))
     assert torch.equal(out, again), "not repeatable"
 
 

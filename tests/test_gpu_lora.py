@@ -48,7 +48,8 @@ def _verify(out, counts, starts, x, W, A, B, scale, ids):
             u, um = mm(x[r][mine] , A[a, e].t())
             u, um = u * scale[a].double(), um * scale[a].double().abs()
             want[mine] += u @ B[a, e].double().t()
-            uerr = (K + 9) * U32 * um + half_ulp(torch.bfloat16) * u.abs() * (1 + 1e-3)   # u as it is used
+            # u as it is used: its own sum, then one rounding to bf16, or to fp32's 24 bits beside an fp32 output
+            uerr = (K + 9) * U32 * um + half_ulp(out.dtype) * u.abs() * (1 + 1e-3)
             babs = B[a, e].double().abs().t()
             extra[mine] += (1 + 1e-3) * uerr @ babs
             mag[mine] += u.abs() @ babs
@@ -64,11 +65,12 @@ def _call(moe, counts, starts, rows, with_counts, out_dtype, x, W, A, B, scale, 
 
 @pytest.mark.parametrize("R", [8, 16, 24, 64, 104, 128])
 @pytest.mark.parametrize("pattern", ["random", "runs"])
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("counts", [[3, 0, 2, 9], [300, 1, 0, 70], [40, 60, 33, 2]], ids=str)
-def test_ranks(moe, R, pattern, counts):
+def test_ranks(moe, R, pattern, out_dtype, counts):
     N, K, L = 328, 264, 5
     a = _inputs(counts, N, K, L, R, pattern, R)
-    out = _call(moe, counts, a[0], a[1], False, "bf16", *a[2:])
+    out = _call(moe, counts, a[0], a[1], False, out_dtype, *a[2:])
     assert moe.moe_get_device_status() == moe.MOE_OK
     _verify(out, counts, a[0], *a[2:])
 
@@ -95,14 +97,17 @@ def test_sizes(moe, size, counts):
     _verify(out, counts, a[0], *a[2:])
 
 
-@pytest.mark.parametrize("counts", [[2000], [900, 0, 1500]], ids=str)
-def test_larger(moe, counts):
-    N, K, L, R = 1032, 904, 7, 64
+@pytest.mark.parametrize("counts", [[2000], [900, 0, 1500], [2500, 700, 1, 1800]], ids=str)
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,K", [(1032, 904), (5120, 328)], ids=str)
+def test_larger(moe, counts, out_dtype, N, K):
+    """Several waves of tiles, narrow and wide, and tiles split over pairs."""
+    L, R = 7, 64
     a = _inputs(counts, N, K, L, R, "runs", 7)
-    out = _call(moe, counts, a[0], a[1], False, "bf16", *a[2:])
+    out = _call(moe, counts, a[0], a[1], False, out_dtype, *a[2:])
     assert moe.moe_get_device_status() == moe.MOE_OK
     _verify(out, counts, a[0], *a[2:])
-    assert torch.equal(out, _call(moe, counts, a[0], a[1], False, "bf16", *a[2:])), "not repeatable"
+    assert torch.equal(out, _call(moe, counts, a[0], a[1], False, out_dtype, *a[2:])), "not repeatable"
 
 
 @pytest.mark.parametrize("counts", [[3, 4], [200, 100]], ids=str)
