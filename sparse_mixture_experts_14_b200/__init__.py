@@ -117,25 +117,40 @@ def _stream(stream=None, *tensors):
     """The stream to launch on: `stream`, else torch's current stream of the device that holds
     the call's CUDA tensors.  Tensors on several devices (or a stream of another device) raise:
     a kernel cannot address another device's memory through them."""
-    devs = {t.device for t in tensors if isinstance(t, torch.Tensor) and t.is_cuda}
-    if len(devs) > 1:
-        raise ValueError(f"tensors on several devices: {sorted(str(v) for v in devs)}")
-    dev = devs.pop() if devs else None
+    dev = -1
+    for t in tensors:
+        if isinstance(t, torch.Tensor):
+            d = t.get_device()   # -1: not a CUDA tensor
+            if d >= 0 and d != dev:
+                if dev >= 0:
+                    devs = {t.device for t in tensors if isinstance(t, torch.Tensor) and t.is_cuda}
+                    raise ValueError(f"tensors on several devices: {sorted(str(v) for v in devs)}")
+                dev = d
+    return _stream_on(stream, dev)
+
+
+# the handle of torch's current stream of a device, without the Stream object around it where torch offers that
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _stream_on(stream, dev):
+    """The handle of `stream`, else of torch's current stream on device index `dev` (-1: the current device)."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif dev is not None and stream.device != dev:
-        raise ValueError(f"stream of {stream.device} for tensors on {dev}")
-    return ctypes.c_void_p(stream.cuda_stream)
+        return _current_stream(dev if dev >= 0 else torch.cuda.current_device())
+    if dev >= 0 and stream.device.index != dev:
+        raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+    return t.data_ptr() if t is not None else None
 
 
 def _dev(t, dtype, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -698,41 +713,54 @@ def moe_grouped_lora(x, W, offsets, A, B, scale, adapter, counts=None, out=None,
     return out
 
 
-class _MoETensor(ctypes.Structure):
-    _fields_ = [("data", _vp), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
-
-
-def _tensor_list(tensors, name):
-    arr = (_MoETensor * max(len(tensors), 1))()
-    for d, t in zip(arr, tensors):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be CUDA tensors")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        d.data, d.numel, d.dtype = t.data_ptr(), t.numel(), _dtype_code(t)
-    return arr
-
-
 def _grad_list(grads):
     """The gradients of a call: a list, or the dict that a backward returns; None entries are left out."""
     return [g for g in (grads.values() if isinstance(grads, dict) else grads) if g is not None]
 
 
-def _norm_tensor(norm, grads):
+_TENSOR_CODES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+
+
+def _tensor_list(tensors, name, dev):
+    """An array of moe_tensor (24 bytes each: address, length, type) and the device index of the tensors,
+    which must be `dev` unless that is -1."""
+    T = torch.Tensor
+    devs = set(map(T.get_device, tensors))   # (a TypeError for what is no tensor)
+    if devs:
+        if min(devs) < 0:
+            raise TypeError(f"{name} must be CUDA tensors")
+        if len(devs | ({dev} if dev >= 0 else set())) > 1:
+            raise ValueError(f"tensors on several devices: {sorted(devs | {dev} - {-1})}")
+        dev = devs.pop()
+    if not all(map(T.is_contiguous, tensors)):
+        raise ValueError(f"{name} must be contiguous")
+    words = [0] * (3 * len(tensors))
+    words[0::3] = map(T.data_ptr, tensors)
+    words[1::3] = map(T.numel, tensors)
+    try:
+        words[2::3] = [_TENSOR_CODES[t.dtype] for t in tensors]
+    except KeyError as e:
+        raise TypeError(f"unsupported dtype {e.args[0]} (bfloat16 or float32)") from None
+    return (ctypes.c_int64 * max(len(words), 1))(*words), dev
+
+
+def _norm_tensor(norm, dev):
     if norm is None:
-        if not grads:
+        if dev < 0:
             raise ValueError("an empty list of gradients needs norm=")
-        norm = torch.empty(1, dtype=torch.float32, device=grads[0].device)
-    _room(norm, 1, "norm")
-    return _dev(norm, torch.float32, "norm")
+        return torch.empty(1, dtype=torch.float32, device=torch.device("cuda", dev)), dev
+    _dev(_room(norm, 1, "norm"), torch.float32, "norm")
+    if dev >= 0 and norm.get_device() != dev:
+        raise ValueError(f"tensors on several devices: cuda:{dev}, {norm.device}")
+    return norm, norm.get_device()
 
 
 def moe_grad_norm(grads, norm=None, stream=None):
     """The global 2-norm of a list (or dict) of gradients, bf16 and float32 mixed: float32 [1] on the device."""
     grads = _grad_list(grads)
-    arr = _tensor_list(grads, "grads")
-    norm = _norm_tensor(norm, grads)
-    _check(_lib.moe_grad_norm(arr, len(grads), _ptr(norm), _stream(stream, norm, *grads)), "moe_grad_norm")
+    arr, dev = _tensor_list(grads, "grads", -1)
+    norm, dev = _norm_tensor(norm, dev)
+    _check(_lib.moe_grad_norm(arr, len(grads), _ptr(norm), _stream_on(stream, dev)), "moe_grad_norm")
     return norm
 
 
@@ -741,15 +769,17 @@ def moe_clip_grads(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
     tensors of `out` (same shapes and types).  Returns (norm float32 [1], the list of clipped tensors).
     No host synchronisation."""
     grads = _grad_list(grads)
-    outs = grads if out is None else _grad_list(out)
-    if len(outs) != len(grads) or any(o.shape != g.shape or o.dtype != g.dtype for o, g in zip(outs, grads)):
-        raise ValueError("out must match the gradients in number, shape and dtype")
-    arr = _tensor_list(grads, "grads")
-    oarr = None if out is None else _tensor_list(outs, "out")
-    norm = _norm_tensor(norm, grads)
-    tensors = grads if out is None else grads + outs
-    _check(_lib.moe_clip_grads(arr, oarr, len(grads), float(max_norm), float(eps), _ptr(norm),
-                               _stream(stream, norm, *tensors)), "moe_clip_grads")
+    outs, oarr = grads, None
+    if out is not None:
+        outs = _grad_list(out)
+        if [o.shape for o in outs] != [g.shape for g in grads]:
+            raise ValueError("out must match the gradients in number and shape")
+    arr, dev = _tensor_list(grads, "grads", -1)
+    if out is not None:
+        oarr, dev = _tensor_list(outs, "out", dev)
+    norm, dev = _norm_tensor(norm, dev)
+    _check(_lib.moe_clip_grads(arr, oarr, len(grads), max_norm, eps, _ptr(norm), _stream_on(stream, dev)),
+           "moe_clip_grads")
     return norm, outs
 
 

@@ -18,6 +18,7 @@ struct Segments {
     const int32_t* counts;    // [E] device or null
     int E;
     int M;                    // rows of the row buffers
+    int least = 0, most = 0x7fffffff;   // segments with fewer or more rows are left to another kernel
 };
 
 // Tiles of `tile` rows: expert e owns tiles [base[e], base[e + 1]).
@@ -42,7 +43,7 @@ __device__ __forceinline__ void build_segments(SegTable* t, const Segments& s, i
             const int n = s.counts ? s.counts[e] : o1 - o0;
             const bool good = o0 >= 0 && o1 >= o0 && o1 <= s.M && n >= 0 && n <= o1 - o0;
             ok = ok && good;
-            tiles = good ? (n + tile - 1) / tile : 0;
+            tiles = good && n >= s.least && n <= s.most ? (n + tile - 1) / tile : 0;
             t->row0[e] = good ? o0 : 0;
             t->rows[e] = good ? n : 0;
         }
@@ -152,7 +153,14 @@ inline LoraView lora_view(const GroupedArgs& a) {
 cudaError_t launch_grouped_simt(const GroupedArgs& a, cudaStream_t s);   // float
 cudaError_t launch_grouped_tc(const GroupedArgs& a, cudaStream_t s);     // bfloat16, M > 0
 cudaError_t launch_grouped_few(const GroupedArgs& a, cudaStream_t s);    // bfloat16 mm with few rows
-bool grouped_few(const GroupedArgs& a);                                  // whether that one is the faster
+
+// Which of the two takes a bf16 mm: the segments with at most `few` rows go to grouped_few, the others to
+// grouped_tc; `both`: the host cannot tell which there are.
+struct Choice {
+    bool few, tc;
+    int limit;
+};
+Choice grouped_choice(const GroupedArgs& a);
 cudaError_t launch_lora_shrink(const GroupedArgs& a, cudaStream_t s);    // u and the tiles' lists
 
 }  // namespace moe

@@ -44,7 +44,16 @@ bool on_device(GroupedArgs* a, int dev) {
 
 cudaError_t launch_product(const GroupedArgs& a, cudaStream_t s) {
     if (!a.in16) return launch_grouped_simt(a, s);
-    return a.op == kGroupedMm && grouped_few(a) ? launch_grouped_few(a, s) : launch_grouped_tc(a, s);
+    const Choice c = grouped_choice(a);
+    GroupedArgs part = a;
+    if (c.few) {
+        if (c.tc) part.seg.most = c.limit;
+        const cudaError_t e = launch_grouped_few(part, s);
+        if (e != cudaSuccess || !c.tc) return e;
+        part.seg.least = c.limit + 1;
+        part.seg.most = a.seg.most;
+    }
+    return launch_grouped_tc(part, s);
 }
 
 moe_status run(GroupedOp op, const void* rows, const void* other, const int32_t* offsets, const int32_t* counts,
@@ -54,7 +63,10 @@ moe_status run(GroupedOp op, const void* rows, const void* other, const int32_t*
     a.rows = rows;
     a.other = other;
     a.out = out;
-    a.seg = {offsets, counts, E, M};
+    a.seg.offsets = offsets;
+    a.seg.counts = counts;
+    a.seg.E = E;
+    a.seg.M = M;
     a.N = N;
     a.K = K;
     a.in16 = dtype == MOE_DTYPE_BF16;
@@ -107,7 +119,10 @@ moe_status moe_grouped_lora(const void* x, const void* W, const int32_t* offsets
     a.rows = x;
     a.other = W;
     a.out = y;
-    a.seg = {offsets, counts, E, M};
+    a.seg.offsets = offsets;
+    a.seg.counts = counts;
+    a.seg.E = E;
+    a.seg.M = M;
     a.N = N;
     a.K = K;
     a.in16 = true;

@@ -53,9 +53,9 @@ __device__ __forceinline__ uint4 load_stream(const __nv_bfloat16* p) {
 }
 
 template <int NT, bool OUT16, bool LORA>
-__global__ void __launch_bounds__(32 * WARPS, NT <= 2 ? 2 : 1) grouped_few_kernel(const FewParams p) {
+__global__ void __launch_bounds__(32 * WARPS, 2) grouped_few_kernel(const FewParams p) {
     constexpr int ROWS = 8 * NT;
-    constexpr int U = NT <= 2 ? 4 : 2;     // steps whose loads are in flight together
+    constexpr int U = 4;                   // steps whose loads are in flight together
     constexpr int PITCH = FEATURES + 1;
     constexpr int TERMS = OUT16 ? 1 : 3;
     __shared__ SegTable seg;
@@ -197,7 +197,9 @@ __global__ void __launch_bounds__(32 * WARPS, NT <= 2 ? 2 : 1) grouped_few_kerne
 
 template <int NT, bool OUT16, bool LORA>
 cudaError_t launch(const GroupedArgs& a, const FewParams& p, cudaStream_t s) {
-    const long long t = (long long)a.seg.M / (8 * NT) + a.seg.E;
+    long long t = (long long)a.seg.M / (8 * NT) + a.seg.E;
+    const long long high = (long long)a.seg.E * ((a.seg.most + 8LL * NT - 1) / (8 * NT));
+    if (t > high) t = high;
     const long long blocks = (t < a.seg.M ? t : a.seg.M) * ((a.N + FEATURES - 1) / FEATURES);
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     return launch_pdl(grouped_few_kernel<NT, OUT16, LORA>, dim3((unsigned)blocks), dim3(32 * WARPS), 0, s, p);
@@ -211,9 +213,17 @@ cudaError_t launch_rows(const GroupedArgs& a, const FewParams& p, cudaStream_t s
 
 }  // namespace
 
-// Up to 8 rows per expert on average, or 32 in all.  Measured (8 experts, 14336 x 4096; us here, us on
-// 256-feature tiles): 8 rows 145, 159; 32 rows 163, 196; 64 rows 187, 198; 128 rows 304, 197.
-bool grouped_few(const GroupedArgs& a) { return a.seg.M <= 32 || a.seg.M <= 8LL * a.seg.E; }
+// Packed segments (no counts): this kernel for up to 8 rows per expert on average, or 32 in all.  Measured
+// (8 experts, 14336 x 4096; us here, us on 256-feature tiles): 8 rows 143, 159; 32 rows 162, 196; 64 rows 178, 198;
+// 128 rows 304, 197.  With counts M is the capacity and says little about the rows (a dispatch pads every
+// expert to 128 and leaves room for 127 more): up to 144 of it per expert both kernels are launched, each for the
+// segments it suits (32 rows in padded segments: 170 us, 194 on 256-feature tiles alone; 256 rows: 213, 197).
+Choice grouped_choice(const GroupedArgs& a) {
+    if (a.op != kGroupedMm) return {false, true, 0};
+    const bool few = a.seg.M <= 32 || a.seg.M <= 8LL * a.seg.E;
+    if (few || !a.seg.counts || a.seg.M > 144LL * a.seg.E) return {few, !few, 0};
+    return {true, true, 16};
+}
 
 cudaError_t launch_grouped_few(const GroupedArgs& a, cudaStream_t s) {
     FewParams p{};
@@ -225,11 +235,11 @@ cudaError_t launch_grouped_few(const GroupedArgs& a, cudaStream_t s) {
     p.K = a.K;
     if (a.A) p.lora = lora_view(a);
     p.status = a.status;
-    // rows of a block: twice the experts' average, so that most segments are one block high
-    const int avg = a.seg.M / a.seg.E;
-    if (a.seg.M <= 8 || avg <= 4) return launch_rows<1>(a, p, s);
-    if (a.seg.M <= 16 || avg <= 8) return launch_rows<2>(a, p, s);
-    return launch_rows<4>(a, p, s);
+    // 8 rows of a segment to a block, or 16 where segments surely have more than a dozen: a second block that
+    // finds the weights in L2 costs less than the wider one's registers (us with 8 and 16: 64 rows of 8 experts
+    // 178, 190; 16 rows of one, 4096 x 4096, 16.4, 18.4; 24 rows 22.5, 18.4).
+    if (a.seg.counts || a.seg.M <= 16LL * a.seg.E) return launch_rows<1>(a, p, s);
+    return launch_rows<2>(a, p, s);
 }
 
 }  // namespace moe

@@ -39,7 +39,7 @@ struct ShrinkParams {
     const __nv_bfloat16* A;
     const float* scale;
     LoraView v;
-    Segments seg;
+    Segments seg, listed;   // all segments; those that grouped_tc takes
     int K;
     int split;     // CTAs of a cluster
     int windows;   // clusters of the first kind along x (an upper bound of the windows)
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(THREADS) lora_shrink_kernel(const ShrinkParams
     const int unit = blockIdx.x / p.split, part = blockIdx.x % p.split;   // cluster, CTA of the cluster
     const bool lists = unit >= p.windows;
     if (lists && (part != 0 || blockIdx.y != 0)) return;
-    if (warp == 0) build_segments(&sm.seg, p.seg, lists ? kColumnTile : WIN, p.status);
+    if (warp == 0) build_segments(&sm.seg, lists ? p.listed : p.seg, lists ? kColumnTile : WIN, p.status);
     __syncthreads();
     const int tile = lists ? unit - p.windows : unit;
     if (tile >= sm.seg.total) return;   // the whole cluster
@@ -252,7 +252,9 @@ cudaError_t launch_lora_shrink(const GroupedArgs& a, cudaStream_t s) {
     p.A = static_cast<const __nv_bfloat16*>(a.A);
     p.scale = a.scale;
     p.v = lora_view(a);
-    p.seg = a.seg;
+    p.seg = p.listed = a.seg;
+    const Choice choice = grouped_choice(a);
+    if (choice.few && choice.tc) p.listed.least = choice.limit + 1;
     p.K = a.K;
     p.status = a.status;
     const int M = a.seg.M, E = a.seg.E, sms = a.num_sms > 0 ? a.num_sms : 148;
