@@ -9,9 +9,7 @@
 // weights' bytes bound the product, as long as no more than the rows' own work is
 // done on them.  The thread groups of a low tile (8 x 4 outputs a thread) split every
 // slice, and where tiles are few, the blocks of a cluster split the reduction; their
-// sums are added through (distributed) shared memory in a fixed order.  In a tile of 128
-// rows the warps whose rows do not exist skip the products (padded segments tell the
-// host nothing about their rows).
+// sums are added through (distributed) shared memory in a fixed order.
 //
 // Operands lie in shared memory with the reduction outermost.  Those that are read along
 // the reduction are turned on the way in; in the low tiles, where the weights' way into
@@ -36,7 +34,8 @@ struct Tile {
     static constexpr int G = THREADS / LANES;             // thread groups
     static constexpr int BK = BM == 128 ? 16 : 32;
     static constexpr int APITCH = BM == 32 ? BM : BM + 4, BPITCH = BM == 128 ? BN + 4 : BN;
-    static constexpr int OPERANDS = BK * (APITCH + BPITCH) * 4;
+    static constexpr int SLICE = BK * (APITCH + BPITCH);   // floats
+    static constexpr int OPERANDS = 2 * SLICE * 4;         // two slices in turn
     static constexpr int SUMS = G * BM * BN * 4;
     static constexpr int SMEM = OPERANDS > SUMS ? OPERANDS : SUMS;
     // the row and the column of a thread's i-th and j-th output
@@ -109,8 +108,6 @@ __global__ void __launch_bounds__(THREADS, 2)
     __shared__ SegTable tab;
     pdl_trigger();
     pdl_wait();
-    float* As = sm;
-    float* Bs = sm + BK * T::APITCH;
     if (threadIdx.x < 32) build_segments(&tab, seg, BM_, blockIdx.x == 0 ? status : nullptr);
     __syncthreads();
     const int part = blockIdx.x % split, tile = blockIdx.x / split;   // CTA of the cluster, cluster
@@ -163,13 +160,14 @@ __global__ void __launch_bounds__(THREADS, 2)
         for (int j = 0; j < T::TN; ++j) acc[i][j] = 0.f;
     const int group = threadIdx.x / T::LANES, lane = threadIdx.x % T::LANES;
     const int tx = lane % (BN / T::TN), ty = lane / (BN / T::TN);
-    // of this thread's rows (warps cover 8 + 8 of a tile of 128): none, the first four, all exist
-    const int live = BM_ != 128 || 64 + (ty & ~1) * 4 < m_rows ? 2 : (ty & ~1) * 4 < m_rows ? 1 : 0;
     if (s0 < s1) {
         a.fetch(s0 * BK);
         b.fetch(s0 * BK);
     }
     for (int s = s0; s < s1; ++s) {
+        // (the slice before the last was read by everyone before the barrier of the last one)
+        float* As = sm + (s & 1) * T::SLICE;
+        float* Bs = As + BK * T::APITCH;
         a.put(As, T::APITCH);
         b.put(Bs, T::BPITCH);
         __syncthreads();
@@ -177,28 +175,23 @@ __global__ void __launch_bounds__(THREADS, 2)
             a.fetch((s + 1) * BK);
             b.fetch((s + 1) * BK);
         }
-        if (live > 0) {
 #pragma unroll
-            for (int i = 0; i < BK / T::G; ++i) {
-                const int c = group * (BK / T::G) + i;
-                float bv[T::TN];
+        for (int i = 0; i < BK / T::G; ++i) {
+            const int c = group * (BK / T::G) + i;
+            float av[T::TM], bv[T::TN];
 #pragma unroll
-                for (int h = 0; h < T::TN; h += 4)
-                    *reinterpret_cast<float4*>(bv + h) =
-                        *reinterpret_cast<const float4*>(Bs + c * T::BPITCH + b.at(T::col(tx, h), c));
+            for (int h = 0; h < T::TM; h += 4)
+                *reinterpret_cast<float4*>(av + h) =
+                    *reinterpret_cast<const float4*>(As + c * T::APITCH + a.at(T::row(ty, h), c));
 #pragma unroll
-                for (int h = 0; h < T::TM; h += 4) {
-                    if (BM_ == 128 && h > 0 && live < 2) break;
-                    const float4 v = *reinterpret_cast<const float4*>(As + c * T::APITCH + a.at(T::row(ty, h), c));
-                    const float av[4] = {v.x, v.y, v.z, v.w};
+            for (int h = 0; h < T::TN; h += 4)
+                *reinterpret_cast<float4*>(bv + h) =
+                    *reinterpret_cast<const float4*>(Bs + c * T::BPITCH + b.at(T::col(tx, h), c));
 #pragma unroll
-                    for (int m = 0; m < 4; ++m)
+            for (int m = 0; m < T::TM; ++m)
 #pragma unroll
-                        for (int n = 0; n < T::TN; ++n) acc[h + m][n] = fmaf(av[m], bv[n], acc[h + m][n]);
-                }
-            }
+                for (int n = 0; n < T::TN; ++n) acc[m][n] = fmaf(av[m], bv[n], acc[m][n]);
         }
-        __syncthreads();
     }
     if (T::G == 1 && split == 1) {
 #pragma unroll
@@ -214,6 +207,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         return;
     }
+    __syncthreads();
     // sums of the thread groups [G][BM][BN], then of the cluster's blocks, which share out the rows
 #pragma unroll
     for (int i = 0; i < T::TM; ++i)
@@ -228,17 +222,23 @@ __global__ void __launch_bounds__(THREADS, 2)
         const int m = u / (BN / 4) * split + part, n = u % (BN / 4) * 4;
         if (m >= m_rows || n >= n_cols) continue;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = 0; c < split; ++c) {
-            const uint32_t at = split > 1 ? ptx::map_to_rank(base, c) : 0u;
+#pragma unroll 1
+        for (int g = 0; g < T::G; ++g) {
+            const int o = (g * BM_ + m) * BN + n;
+            float4 v[MAX_SPLIT];   // all in flight together
 #pragma unroll
-            for (int g = 0; g < T::G; ++g) {
-                const int o = (g * BM_ + m) * BN + n;
-                const float4 v = split > 1 ? ptx::ld_cluster4(at + o * 4) : *reinterpret_cast<const float4*>(sm + o);
-                s.x += v.x;
-                s.y += v.y;
-                s.z += v.z;
-                s.w += v.w;
-            }
+            for (int c = 0; c < MAX_SPLIT; ++c)
+                if (c < split)
+                    v[c] = split > 1 ? ptx::ld_cluster4(ptx::map_to_rank(base + o * 4, c))
+                                     : *reinterpret_cast<const float4*>(sm + o);
+#pragma unroll
+            for (int c = 0; c < MAX_SPLIT; ++c)
+                if (c < split) {
+                    s.x += v[c].x;
+                    s.y += v[c].y;
+                    s.z += v[c].z;
+                    s.w += v[c].w;
+                }
         }
         *reinterpret_cast<float4*>(dst + (size_t)m * ldc + n) = s;
     }
@@ -265,9 +265,17 @@ cudaError_t launch(const GroupedArgs& a, cudaStream_t s) {
         const long long t = (long long)M / BM + E;
         tiles = (t < M ? t : M) * ((ncol + BN - 1) / BN);
     }
-    // split while the blocks leave room on the SMs (two or three fit on one) and each keeps eight slices
+    // the split whose waves of blocks (two to an SM) do the least work each, a little more for every further
+    // part; eight slices a part at least
     int split = 1;
-    while (split < MAX_SPLIT && tiles * split < 2LL * sms && red >= 16 * T::BK * split) split *= 2;
+    float best = 1e30f;
+    for (int s = 1; s <= MAX_SPLIT && (s == 1 || red >= 8 * T::BK * s); s *= 2) {
+        const float cost = (float)((tiles * s + 2 * sms - 1) / (2 * sms)) / s * (1.f + 0.03f * s);
+        if (cost < best) {
+            best = cost;
+            split = s;
+        }
+    }
     if (tiles * split > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
@@ -294,7 +302,8 @@ template <int OP>
 cudaError_t launch_op(const GroupedArgs& a, cudaStream_t s) {
     const int rows = OP == kGroupedWgrad ? a.N : (a.seg.M + a.seg.E - 1) / a.seg.E;
     if (rows <= 8) return launch<OP, 8>(a, s);
-    if (rows <= 48) return launch<OP, 32>(a, s);
+    // (with counts M is a capacity: a dispatch gives every expert 128 rows and room for 127 more)
+    if (rows <= 48 || (OP != kGroupedWgrad && a.seg.counts && rows <= 144)) return launch<OP, 32>(a, s);
     return launch<OP, 128>(a, s);
 }
 

@@ -276,10 +276,11 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
     auto share = [&](const Tile& t) {
         const int slices = LORA ? tile_slices(p.lora, t.col_tile) : 0;
         if (!SPLIT) return Share{0, t.nkb, 0, slices};
-        const long long all = t.nkb + (slices + SLICES - 1) / SLICES;
+        // (a block of adapter slices, which warps prepare by hand, takes the time of about two others)
+        const long long all = t.nkb + 2 * ((slices + SLICES - 1) / SLICES);
         const int b0 = (int)(all * part / parts), b1 = (int)(all * (part + 1) / parts);
-        return Share{min(b0, t.nkb), min(b1, t.nkb), max(b0 - t.nkb, 0) * SLICES,
-                     min(max(b1 - t.nkb, 0) * SLICES, slices)};
+        return Share{min(b0, t.nkb), min(b1, t.nkb), min((max(b0 - t.nkb, 0) + 1) / 2 * SLICES, slices),
+                     min((max(b1 - t.nkb, 0) + 1) / 2 * SLICES, slices)};
     };
     const ptx::WaitCtl wc{&ctrl->abort, p.status, (uint64_t)p.wait_ns};
 

@@ -263,9 +263,9 @@ cudaError_t launch_lora_shrink(const GroupedArgs& a, cudaStream_t s) {
     // split the reduction while the windows leave SMs idle and every part has at least four stages
     p.split = 1;
     while (p.split < MAX_SPLIT && p.windows * p.split < sms && (a.K + KC - 1) / KC >= 8 * p.split) p.split *= 2;
-    // passes side by side: as many as a window can have, no more than fill the SMs a few times over
+    // passes side by side: as many as a window can have, no more than run at once (three blocks to an SM)
     const long long most = ((long long)(a.L < WIN ? a.L : WIN) * p.v.R16 + COLS - 1) / COLS;
-    const long long room = 4LL * sms / ((long long)p.windows * p.split) + 1;
+    const long long room = 3LL * sms / ((long long)p.windows * p.split) + 1;
     static PerDeviceOnce attr;
     cudaError_t e = attr.run([] {
         return cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
