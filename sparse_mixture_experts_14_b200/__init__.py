@@ -17,6 +17,7 @@ gradients of the backward calls.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -723,7 +724,7 @@ _TENSOR_CODES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
 
 def _tensor_list(tensors, name, dev):
     """An array of moe_tensor (24 bytes each: address, length, type) and the device index of the tensors,
-    which must be `dev` unless that is -1."""
+    which must be `dev` unless that is -1.  One pass of C calls per property: lists are long."""
     T = torch.Tensor
     devs = set(map(T.get_device, tensors))   # (a TypeError for what is no tensor)
     if devs:
@@ -738,10 +739,10 @@ def _tensor_list(tensors, name, dev):
     words[0::3] = map(T.data_ptr, tensors)
     words[1::3] = map(T.numel, tensors)
     try:
-        words[2::3] = [_TENSOR_CODES[t.dtype] for t in tensors]
+        words[2::3] = map(_TENSOR_CODES.__getitem__, map(T.dtype.__get__, tensors))
     except KeyError as e:
         raise TypeError(f"unsupported dtype {e.args[0]} (bfloat16 or float32)") from None
-    return (ctypes.c_int64 * max(len(words), 1))(*words), dev
+    return array.array("q", words), dev
 
 
 def _norm_tensor(norm, dev):
@@ -760,26 +761,25 @@ def moe_grad_norm(grads, norm=None, stream=None):
     grads = _grad_list(grads)
     arr, dev = _tensor_list(grads, "grads", -1)
     norm, dev = _norm_tensor(norm, dev)
-    _check(_lib.moe_grad_norm(arr, len(grads), _ptr(norm), _stream_on(stream, dev)), "moe_grad_norm")
+    _check(_lib.moe_grad_norm(arr.buffer_info()[0], len(grads), _ptr(norm), _stream_on(stream, dev)), "moe_grad_norm")
     return norm
 
 
 def moe_clip_grads(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
     """Scale every gradient by min(1, max_norm / (n + eps)), n the global 2-norm: in place, or into the
-    tensors of `out` (same shapes and types).  Returns (norm float32 [1], the list of clipped tensors).
+    tensors of `out` (same lengths and types).  Returns (norm float32 [1], the list of clipped tensors).
     No host synchronisation."""
     grads = _grad_list(grads)
+    arr, dev = _tensor_list(grads, "grads", -1)
     outs, oarr = grads, None
     if out is not None:
         outs = _grad_list(out)
-        if [o.shape for o in outs] != [g.shape for g in grads]:
-            raise ValueError("out must match the gradients in number and shape")
-    arr, dev = _tensor_list(grads, "grads", -1)
-    if out is not None:
-        oarr, dev = _tensor_list(outs, "out", dev)
+        if len(outs) != len(grads):
+            raise ValueError(f"out has {len(outs)} tensors for {len(grads)} gradients")
+        oarr, dev = _tensor_list(outs, "out", dev)   # (the library compares their lengths and types)
     norm, dev = _norm_tensor(norm, dev)
-    _check(_lib.moe_clip_grads(arr, oarr, len(grads), max_norm, eps, _ptr(norm), _stream_on(stream, dev)),
-           "moe_clip_grads")
+    _check(_lib.moe_clip_grads(arr.buffer_info()[0], oarr.buffer_info()[0] if oarr else None, len(grads), max_norm, eps,
+                               _ptr(norm), _stream_on(stream, dev)), "moe_clip_grads")
     return norm, outs
 
 

@@ -136,6 +136,28 @@ def test_overlapping_outputs_are_refused(moe):
     moe.moe_grad_norm([a, b, a])   # reading twice is fine
 
 
+def test_refusals(moe):
+    g, o = [torch.ones(8, device="cuda"), torch.ones(5, device="cuda")], [torch.ones(8, device="cuda")]
+    with pytest.raises(ValueError):
+        moe.moe_clip_grads(g, 1.0, out=o)                                            # another number
+    with pytest.raises(moe.MoEError):
+        moe.moe_clip_grads(g, 1.0, out=o + [torch.ones(4, device="cuda")])           # another length
+    with pytest.raises(moe.MoEError):
+        moe.moe_clip_grads(g, 1.0, out=o + [torch.ones(5, device="cuda").bfloat16()])   # another type
+    with pytest.raises(ValueError):
+        moe.moe_clip_grads([torch.ones(4, 4, device="cuda").t()], 1.0)               # not contiguous
+    with pytest.raises(TypeError):
+        moe.moe_clip_grads([torch.ones(4, device="cuda").half()], 1.0)
+    with pytest.raises(TypeError):
+        moe.moe_clip_grads(g + [torch.ones(4)], 1.0)                                 # on the CPU
+    with pytest.raises(TypeError):
+        moe.moe_clip_grads(g, 1.0, norm=torch.zeros(1, dtype=torch.float64, device="cuda"))
+    for bad in (-1.0, float("nan")):
+        with pytest.raises(moe.MoEError):
+            moe.moe_clip_grads(g, bad)
+    assert all((t == 1).all() for t in g + o)
+
+
 def test_repeatable_on_another_stream_and_in_a_graph(moe):
     grads = _grads(SPECS["lengths"] + [("b", 3_000_000)], seed=4)
     out = [torch.empty_like(g) for g in grads]

@@ -114,5 +114,7 @@ def test_binding_checks():
         moe.moe_clip_grads([], 1.0)
     with pytest.raises(TypeError):
         moe.moe_clip_grads([x], 1.0)
-    with pytest.raises(ValueError):
+    with pytest.raises(TypeError):
         moe.moe_clip_grads([x], 1.0, out=[x[:2]])
+    with pytest.raises(TypeError):
+        moe.moe_clip_grads([3.0], 1.0)
