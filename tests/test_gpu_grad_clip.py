@@ -115,6 +115,41 @@ def test_nan_and_inf(moe, where, dtype):
     assert out[0][where].isnan() and int(out[0].isnan().sum()) == 1 and (out[1] == 0).all()
 
 
+def test_more_than_2_to_31_elements(moe):
+    n = 2 ** 31 + 100_003
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g[5], g[2 ** 31 - 1], g[2 ** 31 + 1], g[n - 1] = 1.0, 2.0, 4.0, 2.0
+    norm, _ = moe.moe_clip_grads([g], 2.5, eps=0.0)
+    assert norm.item() == 5.0
+    for i, want in ((5, 0.5), (2 ** 31 - 1, 1.0), (2 ** 31 + 1, 2.0), (n - 1, 1.0)):
+        assert g[i].item() == want
+    assert int((g != 0).sum()) == 4
+
+
+def test_two_graphs_at_once(moe):
+    """Two captured calls replayed on two streams share nothing."""
+    sets = [_grads(SPECS["lengths"] + [("f", 2_000_003)], seed=s) for s in (8, 9)]
+    graphs, norms = [], [torch.zeros(1, device="cuda") for _ in sets]
+    outs = [[torch.empty_like(g) for g in grads] for grads in sets]
+    moe.moe_clip_grads(sets[0], 0.5, out=outs[0])
+    torch.cuda.synchronize()
+    for grads, out, norm in zip(sets, outs, norms):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            moe.moe_clip_grads(grads, 0.5, out=out, norm=norm)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for grads, out, norm in zip(sets, outs, norms):
+        _check_norm(norm, grads)
+        _check_scaled(out, grads, 0.5, 1e-6)
+
+
 def test_zero_gradients_and_empty_list(moe):
     g = [torch.zeros(5000, device="cuda"), torch.zeros(0, device="cuda", dtype=torch.bfloat16)]
     norm, out = moe.moe_clip_grads(g, 1.0, eps=0.0)

@@ -260,6 +260,33 @@ def test_concurrent_calls_on_two_streams(moe):
         assert torch.equal(a, ref) and torch.equal(b, refd)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("op", ["mm", "dgrad", "wgrad"])
+def test_outputs_past_32_bit_offsets(moe, op, dtype):
+    """More than 2^31 output elements: the last rows (and the first) are right."""
+    small, big = 64, 2 ** 31 // 40000 + 3000
+    rows, N, K = {"mm": (big, 40000, small), "dgrad": (big, small, 40000), "wgrad": (7, 40000, big // 8 * 8)}[op]
+    gen = torch.Generator(device="cuda").manual_seed(20)
+    counts = [rows - 3, 3]
+    starts, _ = segments(counts)
+    off, _ = device_segments(counts, starts, rows, False)
+    x = randn(gen, (rows, K), 1.0, DT[dtype]) if op != "dgrad" else None
+    dy = randn(gen, (rows, N), 1.0, DT[dtype]) if op != "mm" else None
+    W = randn(gen, (2, N, K), 0.1, DT[dtype]) if op != "wgrad" else None
+    out = _run(moe, op, x, dy, W, off, None, None)
+    assert out.numel() > 2 ** 31
+    assert moe.moe_get_device_status() == moe.MOE_OK
+    for e, (s, n) in enumerate(zip(starts, counts)):
+        for part in (slice(0, 64), slice(-64, None)):
+            r = torch.arange(s, s + n, device="cuda")[part]
+            if op == "mm":
+                check(out[r], *mm(x[r], W[e].t()), K, "mm")
+            elif op == "dgrad":
+                check(out[r], *mm(dy[r], W[e]), N, "dgrad")
+            else:
+                check(out[e][part], *mm(dy[s:s + n, part].t(), x[s:s + n]), n, "wgrad")
+
+
 def test_with_the_layers_dispatch(moe):
     """route -> dispatch -> grouped products -> combine is the layer: equal to moe_forward up to the bf16
     rounding of the pre-activations and of the expert outputs, which the fused layer keeps in fp32."""
