@@ -11,8 +11,10 @@
 // the reduction and add their partial sums through distributed shared memory, in
 // CTA order.  Operands go through a 4-stage cp.async ring (64 of the reduction a stage,
 // 128-byte rows with their 16-byte chunks permuted by row) into ldmatrix and
-// mma.m16n8k16.  What bounds it is reading x and the adapters once per window; the
-// split is what gives small batches enough loads in flight.
+// mma.m16n8k16.  What bounds it is reading x and the adapters once per window through L2
+// (4096 rows, 12 adapters of rank 64, K = 4096: 137 MB in 36 us; windows of 128 rows and
+// 128 columns read 83 MB but had 46 us, with half the loads in flight); the split is
+// what gives small batches enough loads in flight (32 rows, 27 pairs of rank 16: 12 us).
 //
 // Further clusters of the same launch write down, for every column tile of the
 // product, the adapters that occur among its rows, each once, in order of first
@@ -268,7 +270,12 @@ cudaError_t launch_lora_shrink(const GroupedArgs& a, cudaStream_t s) {
     const long long room = 3LL * sms / ((long long)p.windows * p.split) + 1;
     static PerDeviceOnce attr;
     cudaError_t e = attr.run([] {
-        return cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        // (three blocks to an SM need nearly all of its shared memory)
+        const cudaError_t r = cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                   cudaSharedmemCarveoutMaxShared);
+        return r != cudaSuccess ? r
+                                : cudaFuncSetAttribute(lora_shrink_kernel,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
