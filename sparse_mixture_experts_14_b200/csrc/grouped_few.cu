@@ -105,6 +105,15 @@ __global__ void __launch_bounds__(32 * WARPS, 2) grouped_few_kernel(const FewPar
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[i][t][c] = 0.f;
+    if (LORA) {
+        // the adapters' rows of B that this thread's outputs need, on their way to L2 meanwhile
+        for (int o = tid; o < rows * FEATURES; o += 32 * WARPS) {
+            const int id = p.lora.adapter[row0 + o / FEATURES], f = f0 + o % FEATURES;
+            if (f >= N || id < 0 || id >= p.lora.L) continue;
+            const __nv_bfloat16* bl = p.lora.B + (((size_t)id * p.seg.E + e) * N + f) * p.lora.R;
+            for (int j = 0; j < p.lora.R; j += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(bl + j));
+        }
+    }
     for (int k0 = warp * 32; k0 < K; k0 += WARPS * 32 * U) {
         uint4 a[U][MT][2], b[U][NT];
 #pragma unroll

@@ -22,7 +22,7 @@
 // A pair of CTAs computes a 256 x (up to 256) tile with tcgen05.mma.cta_group::2,
 // each CTA holding 128 features and half of the columns' operand.  Persistent, one
 // CTA per SM: warp 0 TMA producer into a ring of 64-deep stages, warp 1 MMA issuer
-// (in the pair's leader), 8 or 16 epilogue warps for the CTA's 128 features out of two
+// (in the pair's leader), 16 epilogue warps for the CTA's 128 features out of two
 // alternating accumulators, a further warp for the ends of wgrad's segments.
 //
 // fp32 outputs: the tensor cores truncate when they add to the accumulator, which
@@ -121,8 +121,8 @@ struct Cfg {
     static constexpr bool A_MN = OP != kGroupedMm;
     static constexpr bool B_MN = WGRAD;
     static constexpr int AUX_WARPS = WGRAD ? 1 : LORA ? 2 : 0;
-    static constexpr int EPI_WARPS = OUT16 && W == 1 ? 8 : 16;
-    static constexpr int COLS = OUT16 ? 128 : 64;   // columns of an epilogue warp
+    static constexpr int EPI_WARPS = 16;
+    static constexpr int COLS = W == 2 ? 128 : 64;   // columns of an epilogue warp
     static constexpr int THREADS = 32 * (2 + EPI_WARPS + AUX_WARPS);
     static constexpr int NST = W == 1 ? 6 : 4;
     static constexpr int STAGE = W * A_BYTES + B_BYTES;

@@ -270,12 +270,9 @@ cudaError_t launch_lora_shrink(const GroupedArgs& a, cudaStream_t s) {
     const long long room = 3LL * sms / ((long long)p.windows * p.split) + 1;
     static PerDeviceOnce attr;
     cudaError_t e = attr.run([] {
-        // (three blocks to an SM need nearly all of its shared memory)
-        const cudaError_t r = cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                                   cudaSharedmemCarveoutMaxShared);
-        return r != cudaSuccess ? r
-                                : cudaFuncSetAttribute(lora_shrink_kernel,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        // (the carveout stays the default: with all of an SM's memory given to shared memory for this kernel, the
+        // weight-streaming product beside it lost its L1 and took 231 us instead of 183)
+        return cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
