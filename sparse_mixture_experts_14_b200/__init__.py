@@ -705,6 +705,8 @@ def moe_grouped_lora(x, W, offsets, A, B, scale, adapter, counts=None, out=None,
     if workspace is None:
         workspace = torch.empty(max(moe_grouped_lora_workspace_size(M, E, L, R), 1), dtype=torch.uint8,
                                 device=x.device)
+        if stream is not None and workspace.is_cuda:
+            workspace.record_stream(stream)   # it is freed on return, while `stream` may still use it
     _dev(workspace, torch.uint8, "workspace")
     _check(_lib.moe_grouped_lora(_ptr(x), _ptr(W), _ptr(offsets), _ptr(counts), _ptr(A), _ptr(B), _ptr(scale),
                                  _ptr(adapter), _ptr(out), M, N, K, E, L, R, ocode, _ptr(workspace),

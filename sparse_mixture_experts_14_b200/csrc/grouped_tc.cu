@@ -8,9 +8,9 @@
 // the MMA's M side, so that the 32 lanes of an epilogue warp hold 32 neighbours
 // in memory, and the output's rows ("columns" of the accumulator: tokens, tokens,
 // dW's n) on its N side.  The N side is where segments are ragged, and N is an
-// instruction field: a segment of n rows is cut into ceil(n / 256) tiles of equal
-// height, rounded up to 32, so that no more than 31 rows a tile are computed in
-// vain (a 256-row M side would round every segment up to 256).
+// instruction field: a segment is cut into nearly equal tiles of up to 256 rows
+// (column_tiles), which compute at most 31 rows in vain (a 256-row M side would round
+// every segment up to 256).
 //
 //              M side (A)                     N side (B)                reduction
 //     mm       W_e  [f][K]    K-major         x rows   K-major          K
@@ -30,7 +30,7 @@
 // reduction of 14336, where a blocked fp32 sum has 3e-7).  So the accumulator takes
 // 512 of the reduction at a time, and the epilogue adds these partial sums in
 // registers with rounding, while the MMAs go on in the other accumulator.  bf16
-// outputs, whose own rounding is 2^-9, take the whole reduction in one.
+// outputs, whose own rounding is 2^-8, take the whole reduction in one.
 //
 // Adapters (lora.cu computes u_r = s_a A_{a,e} x_r, bf16): B_{a,e} u_r is more of the
 // same reduction.  For every adapter that occurs among a tile's rows, in slices of 16
@@ -162,15 +162,15 @@ __device__ __forceinline__ Tile decode(const Ctrl* c, const Params& p, int tile)
         const int local = tile - c->seg.base[t.e] * nf;
         const int fi = local / tt;
         t.rows = c->seg.rows[t.e];
-        const int h = column_tile_height(t.rows);
-        const int r = (local - fi * tt) * h;
+        const ColumnTiles ct = column_tiles(t.rows);
+        const int i = local - fi * tt, r = ct.start(i);
         t.f0 = fi * PAIR_F;
         t.row0 = c->seg.row0[t.e];
         t.c0 = t.row0 + r;
-        t.valid = min(h, t.rows - r);
-        t.nn = h;
+        t.nn = ct.rows(i);
+        t.valid = min(t.nn, t.rows - r);
         t.nkb = (p.red + BK - 1) / BK;
-        t.col_tile = c->seg.base[t.e] + (local - fi * tt);
+        t.col_tile = c->seg.base[t.e] + i;
     }
     return t;
 }
@@ -372,16 +372,16 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                         ptx::mbar_arrive(&ctrl->land[stage]);   // the stage is free: u's warps may write it
                         const uint32_t bar = ptx::map_to_rank(ptx::smem_addr(&ctrl->full[stage]), lead);
                         if (leader) ptx::mbar_arrive_expect_tx(&ctrl->full[stage], 2 * n * W * SLICE_BYTES);
-                        const int step = p.lora.box / SLICE;
+                        const int step = p.lora.box / SLICE, ranks = p.lora.R16 / SLICE;
 #pragma unroll
                         for (int i = 0; i < SLICES; ++i) {
                             if (i >= n) break;
                             if (i % step != 0) continue;
+                            const int k = (s0 + i) % per % ranks * SLICE;
 #pragma unroll
                             for (int h = 0; h < W; ++h)
                                 ptx::tma_load_3d_pair(smem + stage * STAGE + h * A_BYTES + i * SLICE_BYTES, &maps.l, bar,
-                                                      (s0 + i) % per % (p.lora.R16 / SLICE) * SLICE, fa + h * 2 * BM, z[i] * p.seg.E + t.e,
-                                                      pol);
+                                                      k, fa + h * 2 * BM, z[i] * p.seg.E + t.e, pol);
                         }
 #pragma unroll
                         for (int i = 0; i < SLICES; ++i) z[i] = list[min(s0 + SLICES + i, sh.s1 - 1) / per];
@@ -727,7 +727,8 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                 const int r = t0 + 64 * j, col = (int)rank * (t.nn / 2) + r;
                 const bool live = r < t.nn / 2 && col < t.valid;
                 id[j] = live ? p.lora.adapter[(size_t)t.c0 + col] : -1;
-                u[j] = reinterpret_cast<const uint4*>(p.lora.u + ((size_t)t.c0 + (live ? col : 0)) * p.lora.terms * p.lora.R16);
+                u[j] = reinterpret_cast<const uint4*>(
+                    p.lora.u + ((size_t)t.c0 + (live ? col : 0)) * p.lora.terms * p.lora.R16);
             }
             // the rows' part of four slices: read ahead of the wait for the stage
             uint4 v[SLICES][2][2];

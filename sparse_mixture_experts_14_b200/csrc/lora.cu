@@ -126,8 +126,9 @@ __global__ void __launch_bounds__(THREADS) lora_shrink_kernel(const ShrinkParams
     const int tile = lists ? unit - p.windows : unit;
     if (tile >= sm.seg.total) return;   // the whole cluster
     const int e = segment_of(&sm.seg, p.seg.E, tile);
-    const int rows = sm.seg.rows[e], h = lists ? column_tile_height(rows) : WIN;
-    const int r0 = (tile - sm.seg.base[e]) * h, n = min(h, rows - r0);
+    const int rows = sm.seg.rows[e], at = tile - sm.seg.base[e];
+    const ColumnTiles ct = column_tiles(rows);
+    const int r0 = lists ? ct.start(at) : at * WIN, n = min(lists ? ct.rows(at) : WIN, rows - r0);
     const size_t row0 = (size_t)sm.seg.row0[e] + r0;
     if (tid < n) sm.ids[tid] = adapter_of(p, row0 + tid);
     __syncthreads();
