@@ -577,24 +577,21 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                     odd = !(__low2float(t2) == 0.f && __high2float(t2) == 0.f);
                     odd = __any_sync(0xffffffffu, odd);
                 }
-                // A lane holds one feature of columns i and i + 1; lanes 0-15 gather pairs of features of column
-                // i, lanes 16-31 of column i + 1, so that neighbouring lanes write neighbouring bytes (with the
-                // columns on alternating lanes every 32-byte sector went to L2 in several pieces: 3.7 times
-                // the output's sectors instead of 1.5).  F is a multiple of 8: pairs are whole.
-                const int hi = lane >> 4, src = 2 * (lane & 15);
-                const int fp = t.f0 + blk * 2 * BM + (int)rank * BM + q * 32 + src;
+                // Neighbouring lanes swap halves: of columns i and i + 1 the even lane stores features f, f + 1 of
+                // the first, the odd one f - 1, f of the second.  F is a multiple of 8: pairs are whole.
+                const int hi = lane & 1;
+                const int fp = t.f0 + blk * 2 * BM + (int)rank * BM + q * 32 + (lane & ~1);
                 __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (row0 + hi) * p.F + fp;
-                const uint32_t sel = hi ? 0x7632u : 0x5410u;
+                const uint32_t sel = hi ? 0x3276u : 0x5410u;
                 const int cols = (fp < p.F ? t.valid - c0 : 0) - hi;
 #pragma unroll
                 for (int c = 0; c < CF::COLS; c += 16) {
                     if (c >= ncol) break;
 #pragma unroll
                     for (int i = c; i < c + 16; i += 2) {
-                        const uint32_t a = __shfl_sync(0xffffffffu, v[i / 2], src);
-                        const uint32_t b = __shfl_sync(0xffffffffu, v[i / 2], src + 1);
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, v[i / 2], 1);
                         if (i < cols)
-                            *reinterpret_cast<uint32_t*>(out + (size_t)(i - c) * p.F) = __byte_perm(a, b, sel);
+                            *reinterpret_cast<uint32_t*>(out + (size_t)(i - c) * p.F) = __byte_perm(v[i / 2], got, sel);
                     }
                     out += 16 * (size_t)p.F;
                     asm volatile("" : "+l"(out));   // one pointer, not one per column, in registers
