@@ -619,11 +619,20 @@ def _segment_args(offsets, counts):
     return E
 
 
-def _grouped_out(out, shape, dtype, like):
+def _empty(shape, dtype, device, stream):
+    """A tensor for a call on `stream` (None: the current one), from that stream's memory: from the current
+    stream's it could still be in use there, or be in use again before `stream` is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _grouped_out(out, shape, dtype, like, stream):
     """The output tensor of a grouped product: the caller's, of exactly `shape` (rows in no segment keep
     what it holds), or a new one."""
     if out is None:
-        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+        return _empty(shape, dtype or like.dtype, like.device, stream)
     if not isinstance(out, torch.Tensor) or tuple(out.shape) != tuple(shape):
         raise ValueError(f"out must have shape {tuple(shape)}")
     if dtype is not None and out.dtype != dtype:
@@ -651,7 +660,7 @@ def moe_grouped_mm(x, W, offsets, counts=None, out=None, out_dtype=None, stream=
     if x.dim() != 2 or W.dim() != 3 or W.shape[0] != E or W.shape[2] != x.shape[1]:
         raise ValueError(f"inconsistent shapes x{tuple(x.shape)} W{tuple(W.shape)} for {E} segments")
     (M, K), N = x.shape, W.shape[1]
-    out = _grouped_out(out, (M, N), out_dtype, x)
+    out = _grouped_out(out, (M, N), out_dtype, x, stream)
     return _grouped("moe_grouped_mm", x, W, "x", "W", offsets, counts, out, M, N, K, E, stream)
 
 
@@ -661,7 +670,7 @@ def moe_grouped_dgrad(dy, W, offsets, counts=None, out=None, out_dtype=None, str
     if dy.dim() != 2 or W.dim() != 3 or W.shape[0] != E or W.shape[1] != dy.shape[1]:
         raise ValueError(f"inconsistent shapes dy{tuple(dy.shape)} W{tuple(W.shape)} for {E} segments")
     (M, N), K = dy.shape, W.shape[2]
-    out = _grouped_out(out, (M, K), out_dtype, dy)
+    out = _grouped_out(out, (M, K), out_dtype, dy, stream)
     return _grouped("moe_grouped_dgrad", dy, W, "dy", "W", offsets, counts, out, M, N, K, E, stream)
 
 
@@ -672,7 +681,7 @@ def moe_grouped_wgrad(dy, x, offsets, counts=None, out=None, out_dtype=None, str
     if dy.dim() != 2 or x.dim() != 2 or x.shape[0] != dy.shape[0]:
         raise ValueError(f"inconsistent shapes dy{tuple(dy.shape)} x{tuple(x.shape)}")
     (M, N), K = dy.shape, x.shape[1]
-    out = _grouped_out(out, (E, N, K), out_dtype, dy)
+    out = _grouped_out(out, (E, N, K), out_dtype, dy, stream)
     return _grouped("moe_grouped_wgrad", dy, x, "dy", "x", offsets, counts, out, M, N, K, E, stream)
 
 
@@ -699,14 +708,11 @@ def moe_grouped_lora(x, W, offsets, A, B, scale, adapter, counts=None, out=None,
         _dev(t, torch.bfloat16, n)
     _dev(scale, torch.float32, "scale")
     _dev(adapter, torch.int32, "adapter")
-    out = _grouped_out(out, (M, N), out_dtype, x)
+    out = _grouped_out(out, (M, N), out_dtype, x, stream)
     ocode = _dtype_code(out)
     _dev(out, out.dtype, "out")
     if workspace is None:
-        workspace = torch.empty(max(moe_grouped_lora_workspace_size(M, E, L, R), 1), dtype=torch.uint8,
-                                device=x.device)
-        if stream is not None and workspace.is_cuda:
-            workspace.record_stream(stream)   # it is freed on return, while `stream` may still use it
+        workspace = _empty(max(moe_grouped_lora_workspace_size(M, E, L, R), 1), torch.uint8, x.device, stream)
     _dev(workspace, torch.uint8, "workspace")
     _check(_lib.moe_grouped_lora(_ptr(x), _ptr(W), _ptr(offsets), _ptr(counts), _ptr(A), _ptr(B), _ptr(scale),
                                  _ptr(adapter), _ptr(out), M, N, K, E, L, R, ocode, _ptr(workspace),
@@ -717,8 +723,11 @@ def moe_grouped_lora(x, W, offsets, A, B, scale, adapter, counts=None, out=None,
 
 
 def _grad_list(grads):
-    """The gradients of a call: a list, or the dict that a backward returns; None entries are left out."""
-    return [g for g in (grads.values() if isinstance(grads, dict) else grads) if g is not None]
+    """The gradients of a call: a list, or the dict that a backward returns without its gradients of rows (dx,
+    dh), which are no parameters'; None entries are left out."""
+    if isinstance(grads, dict):
+        grads = [g for n, g in grads.items() if n not in ("dx", "dh")]
+    return [g for g in grads if g is not None]
 
 
 _TENSOR_CODES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
@@ -747,11 +756,11 @@ def _tensor_list(tensors, name, dev):
     return array.array("q", words), dev
 
 
-def _norm_tensor(norm, dev):
+def _norm_tensor(norm, dev, stream):
     if norm is None:
         if dev < 0:
             raise ValueError("an empty list of gradients needs norm=")
-        return torch.empty(1, dtype=torch.float32, device=torch.device("cuda", dev)), dev
+        return _empty(1, torch.float32, torch.device("cuda", dev), stream), dev
     _dev(_room(norm, 1, "norm"), torch.float32, "norm")
     if dev >= 0 and norm.get_device() != dev:
         raise ValueError(f"tensors on several devices: cuda:{dev}, {norm.device}")
@@ -759,10 +768,11 @@ def _norm_tensor(norm, dev):
 
 
 def moe_grad_norm(grads, norm=None, stream=None):
-    """The global 2-norm of a list (or dict) of gradients, bf16 and float32 mixed: float32 [1] on the device."""
+    """The global 2-norm of a list of gradients, bf16 and float32 mixed: float32 [1] on the device.  The dict of
+    moe_backward_ws or moe_block_backward_ws is taken without its dx or dh."""
     grads = _grad_list(grads)
     arr, dev = _tensor_list(grads, "grads", -1)
-    norm, dev = _norm_tensor(norm, dev)
+    norm, dev = _norm_tensor(norm, dev, stream)
     _check(_lib.moe_grad_norm(arr.buffer_info()[0], len(grads), _ptr(norm), _stream_on(stream, dev)), "moe_grad_norm")
     return norm
 
@@ -770,7 +780,8 @@ def moe_grad_norm(grads, norm=None, stream=None):
 def moe_clip_grads(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
     """Scale every gradient by min(1, max_norm / (n + eps)), n the global 2-norm: in place, or into the
     tensors of `out` (same lengths and types).  Returns (norm float32 [1], the list of clipped tensors).
-    No host synchronisation."""
+    The dict of moe_backward_ws or moe_block_backward_ws is taken without its dx or dh.  No host
+    synchronisation."""
     grads = _grad_list(grads)
     arr, dev = _tensor_list(grads, "grads", -1)
     outs, oarr = grads, None
@@ -779,7 +790,7 @@ def moe_clip_grads(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
         if len(outs) != len(grads):
             raise ValueError(f"out has {len(outs)} tensors for {len(grads)} gradients")
         oarr, dev = _tensor_list(outs, "out", dev)   # (the library compares their lengths and types)
-    norm, dev = _norm_tensor(norm, dev)
+    norm, dev = _norm_tensor(norm, dev, stream)
     _check(_lib.moe_clip_grads(arr.buffer_info()[0], oarr.buffer_info()[0] if oarr else None, len(grads), max_norm, eps,
                                _ptr(norm), _stream_on(stream, dev)), "moe_clip_grads")
     return norm, outs

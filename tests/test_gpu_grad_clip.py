@@ -202,7 +202,11 @@ def test_repeatable_on_another_stream_and_in_a_graph(moe):
     with torch.cuda.stream(side):
         out2 = [torch.empty_like(g) for g in grads]
         norm2, _ = moe.moe_clip_grads(grads, 0.5, out=out2)
+        norm3 = moe.moe_grad_norm(grads)
+    norm4, out4 = moe.moe_clip_grads(grads, 0.5, out=[torch.empty_like(g) for g in grads], stream=side)
     side.synchronize()
+    assert torch.equal(norm, norm3) and torch.equal(norm, norm4)
+    assert all(torch.equal(a, b) for a, b in zip(out, out4))
     assert torch.equal(norm, norm2) and all(torch.equal(a, b) for a, b in zip(out, out2))
     g = torch.cuda.CUDAGraph()
     nrm = torch.zeros(1, device="cuda")
@@ -227,9 +231,10 @@ def test_after_the_layers_backward(moe, dtype):
     ws = torch.empty(moe.moe_train_workspace_size(T, d, F, E, k, code), dtype=torch.uint8, device="cuda")
     moe.moe_forward_ws(*args, k, path=moe.MOE_PATH_TRAIN, workspace=ws)
     g, _ = moe.moe_backward_ws(*args, to_dev(moe_inputs.make_dout(T, d, dtype, seed=41), dtype), k, ws)
-    dx = g.pop("dx").clone()
-    keep = [t.clone() for t in g.values()]
+    dx = g["dx"].clone()
+    keep = [t.clone() for n, t in g.items() if n != "dx"]
     norm, clipped = moe.moe_clip_grads(g, 0.1)
+    assert len(clipped) == len(keep) and torch.equal(g["dx"], dx)   # the rows' gradient is no parameter's
     _check_norm(norm, keep)
-    _check_scaled(list(g.values()), keep, 0.1, 1e-6)
-    assert torch.isfinite(dx).all() and moe.moe_get_device_status() == moe.MOE_OK
+    _check_scaled(clipped, keep, 0.1, 1e-6)
+    assert moe.moe_get_device_status() == moe.MOE_OK

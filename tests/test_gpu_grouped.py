@@ -97,6 +97,17 @@ def test_odd_sizes(moe, op, types, size, seg):
 
 
 @pytest.mark.parametrize("op", ["mm", "dgrad", "wgrad"])
+@pytest.mark.parametrize("size", [(4, 12), (12, 4), (132, 4), (4, 1028)], ids=str)
+@pytest.mark.parametrize("seg", ["tiles", "few-rows", "padded"])
+def test_smallest_steps_fp32(moe, op, size, seg):
+    N, K = size
+    counts, starts, rows, off, cnt, x, dy, W = _inputs(seg, N, K, "f32", 21)
+    out = _run(moe, op, x, dy, W, off, cnt, _out(op, rows, len(counts), N, K, "f32"))
+    assert moe.moe_get_device_status() == moe.MOE_OK
+    _verify(op, out, counts, starts, x, dy, W)
+
+
+@pytest.mark.parametrize("op", ["mm", "dgrad", "wgrad"])
 @pytest.mark.parametrize("counts", [[1500, 0, 2600, 900], [9, 8, 0, 7], [60, 200, 2, 90]], ids=str)
 @pytest.mark.parametrize("N,K", [(2056, 1736), (5120, 640), (1024, 4608)], ids=str)
 @pytest.mark.parametrize("out_dtype", ["bf16", "f32"])

@@ -173,6 +173,23 @@ def test_graph_reads_ids_at_replay(moe, counts):
     assert moe.moe_get_device_status() == moe.MOE_OK
 
 
+@pytest.mark.parametrize("counts", [[5, 4], [300, 90]], ids=str)
+def test_two_calls_at_once(moe, counts):
+    """On two streams, with scratch of their own (the binding's, allocated on the stream of the call)."""
+    starts, rows, x, W, A, B, scale, ids = _inputs(counts, 776, 520, 6, 32, "random", 12)
+    off, _ = device_segments(counts, starts, rows, False)
+    ids2 = ids.flip(0).contiguous()
+    refs = [moe.moe_grouped_lora(x, W, off, A, B, scale, i) for i in (ids, ids2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [[moe.moe_grouped_lora(x, W, off, A, B, scale, i, stream=s) for i, s in zip((ids, ids2), streams)]
+            for _ in range(8)]
+    torch.cuda.synchronize()
+    assert moe.moe_get_device_status() == moe.MOE_OK
+    for pair in outs:
+        assert torch.equal(pair[0], refs[0]) and torch.equal(pair[1], refs[1])
+
+
 def test_adapters_on_the_layers_experts(moe):
     """A served batch: route, dispatch, adapters of every request on all three expert matrices, combine."""
     import moe_inputs
