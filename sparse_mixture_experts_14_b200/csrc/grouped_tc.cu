@@ -731,52 +731,45 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                 u[j] = reinterpret_cast<const uint4*>(
                     p.lora.u + ((size_t)t.c0 + (live ? col : 0)) * p.lora.terms * p.lora.R16);
             }
-            // the rows' part of four slices: read ahead of the wait for the stage
-            uint4 v[SLICES][2][2];
-            auto fetch = [&](int s0) {
-                const int n = min(SLICES, slices - s0);
-#pragma unroll
-                for (int i = 0; i < SLICES; ++i) {
-                    const int k = (s0 + i) / per;
-                    const int h = __shfl_sync(0xffffffffu, head, k & 31);
-                    const int a = i >= n ? -2 : k < 32 ? h : list[k];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        v[i][j][0] = v[i][j][1] = make_uint4(0, 0, 0, 0);
-                        if (id[j] == a) {
-                            v[i][j][0] = u[j][2 * ((s0 + i) % per)];
-                            v[i][j][1] = u[j][2 * ((s0 + i) % per) + 1];
-                        }
-                    }
-                }
-            };
-            if (sh.s0 < slices) fetch(sh.s0);
+            // copies of a stage go out as soon as it is free; the stage before is then waited for and handed over
             block += sh.kb1 - sh.kb0;
+            auto hand_over = [&](unsigned blk) {
+                ptx::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive_operands(ptx::map_to_rank(ptx::smem_addr(&ctrl->ready[blk % NST]), lead));
+            };
             for (int s0 = sh.s0; s0 < slices; s0 += SLICES, ++block) {
-                const int stage = block % NST;
+                const int stage = block % NST, n = min(SLICES, slices - s0);
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(&ctrl->land[stage], land_phase >> stage & 1, wc));
                 if (!ok) break;
                 land_phase ^= 1u << stage;
-                uint8_t* sb = smem + stage * STAGE + W * A_BYTES;
+                const uint32_t sb = ptx::smem_addr(smem + stage * STAGE + W * A_BYTES);
 #pragma unroll
                 for (int i = 0; i < SLICES; ++i) {
-                    if (i >= slices - s0) break;
+                    if (i >= n) break;
+                    const int k = (s0 + i) / per, part16 = (s0 + i) % per;
+                    const int h = __shfl_sync(0xffffffffu, head, k & 31);
+                    const int a = k < 32 ? h : list[k];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int r = t0 + 64 * j;
                         if (r >= t.nn / 2) continue;
                         // box i / step, rows of 2 box bytes whose 16-byte chunks are permuted by row as TMA does
                         const int chunk = i % step * 2, x = swizzle(r, box);
-                        uint8_t* row = sb + i / step * step * SLICE_BYTES + r * 2 * box;
-                        *reinterpret_cast<uint4*>(row + (chunk ^ x) * 16) = v[i][j][0];
-                        *reinterpret_cast<uint4*>(row + ((chunk + 1) ^ x) * 16) = v[i][j][1];
+                        const uint32_t row = sb + i / step * step * SLICE_BYTES + r * 2 * box;
+                        ptx::cp_async16(row + (chunk ^ x) * 16, u[j] + 2 * part16, id[j] == a);
+                        ptx::cp_async16(row + ((chunk + 1) ^ x) * 16, u[j] + 2 * part16 + 1, id[j] == a);
                     }
                 }
-                ptx::fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_operands(ptx::map_to_rank(ptx::smem_addr(&ctrl->ready[stage]), lead));
-                if (s0 + SLICES < slices) fetch(s0 + SLICES);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (s0 > sh.s0) {
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    hand_over(block - 1);
+                }
             }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            if (ok && sh.s0 < slices) hand_over(block - 1);
         }
     }
 

@@ -73,11 +73,6 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                  : "memory");
 }
 
-// 16 bytes to shared memory; zeros where !live (src is then not read).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-
 // The distinct ids of ids[0, n), in order of first occurrence, into list; sm->n of them (all threads).
 __device__ __forceinline__ void distinct(ShrinkSmem* sm, int n) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -166,7 +161,7 @@ __global__ void __launch_bounds__(THREADS) lora_shrink_kernel(const ShrinkParams
             for (int j = 0; j < 4; ++j) {
                 const int r = lrow + 32 * (j & 1);
                 const bool live = in && src[j];
-                cp_async16(stage + (j >> 1) * TILE_BYTES + r * 128 + ((lchunk ^ (r & 7)) * 16),
+                ptx::cp_async16(stage + (j >> 1) * TILE_BYTES + r * 128 + ((lchunk ^ (r & 7)) * 16),
                            live ? src[j] + (size_t)kb * KC : p.x, live);
             }
         };

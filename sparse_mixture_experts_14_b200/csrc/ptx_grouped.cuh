@@ -41,5 +41,10 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
     return v;
 }
 
+// 16 bytes to shared memory; zeros where !live (src is then not read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
 }  // namespace ptx
 }  // namespace moe
