@@ -174,6 +174,32 @@ def test_graph_reads_ids_at_replay(moe, counts):
 
 
 @pytest.mark.parametrize("counts", [[5, 4], [300, 90]], ids=str)
+def test_inputs_written_just_before_the_call(moe, counts):
+    """Rows, ids, offsets and weights that kernels still in flight write: the call's kernels start early and
+    must wait for them."""
+    starts, rows, x, W, A, B, scale, ids = _inputs(counts, 776, 520, 6, 32, "random", 13)
+    off, _ = device_segments(counts, starts, rows, False)
+    big = torch.randn(4096, 4096, device="cuda")
+    want = moe.moe_grouped_lora(x, W, off, A, B, scale, ids)
+    live = [torch.zeros_like(t) for t in (x, W, off, A, B, scale, ids)]
+    for i in range(6):
+        for t in live:
+            t.zero_()
+        out = torch.full_like(want, SENTINEL)
+        torch.cuda.synchronize()
+        busy = big @ big   # something to wait behind
+        for t, v in zip(live, (x, W, off, A, B, scale, ids)):
+            t.copy_(v)
+        lx, lW, loff, lA, lB, lscale, lids = live
+        moe.moe_grouped_lora(lx, lW, loff, lA, lB, lscale, lids, out=out)
+        lx.zero_()         # and nothing after the call is too early
+        lB.zero_()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), i
+    assert moe.moe_get_device_status() == moe.MOE_OK and torch.isfinite(busy).all()
+
+
+@pytest.mark.parametrize("counts", [[5, 4], [300, 90]], ids=str)
 def test_two_calls_at_once(moe, counts):
     """On two streams, with scratch of their own (the binding's, allocated on the stream of the call)."""
     starts, rows, x, W, A, B, scale, ids = _inputs(counts, 776, 520, 6, 32, "random", 12)
