@@ -11,8 +11,9 @@
 // slice, and where tiles are few, the blocks of a cluster split the reduction; their
 // sums are added through (distributed) shared memory in a fixed order.
 //
-// Measured: 6296 rows of 7 experts, 1416 x 1264, 0.62 ms (36 TFLOP/s, as the library's fp32 product);
-// 1003 rows of 5, 86 us.
+// Measured: 6296 rows of 7 experts, 1416 x 1264, 0.57 ms (0.67 with a product to an instruction); 1003 rows
+// of 5, 80 us; weight gradients of 8192 rows, 4 experts of 2048 x 1024, 0.72 ms (48 TFLOP/s; 0.92 with one).
+// What bounds it is the multiply-adds, and the last wave of blocks where it is not full.
 //
 // Operands lie in shared memory with the reduction outermost.  Those that are read along
 // the reduction are turned on the way in; in the low tiles, where the weights' way into
@@ -41,6 +42,12 @@ struct Tile {
     static constexpr int OPERANDS = 2 * SLICE * 4;         // two slices in turn
     static constexpr int SUMS = G * BM * BN * 4;
     static constexpr int SMEM = OPERANDS > SUMS ? OPERANDS : SUMS;
+    // Two products to an instruction (fma.rn.f32x2): of neighbouring columns, or of neighbouring rows.  The
+    // other factor is doubled on the way, so the fewer of those the better (200 rows of 8 experts, 4096 x 2048:
+    // 176 us in columns, 160 in rows); the high tile has as many of either and fewer registers to spare in rows
+    // (6296 rows of 7, 1416 x 1264: 569 in columns, 610 in rows).
+    static constexpr bool COLS = BM == 128;
+    static constexpr int AM = COLS ? TM : TM / 2, AN = COLS ? TN / 2 : TN;   // a thread's sums, in pairs
     // the row and the column of a thread's i-th and j-th output
     __device__ static int row(int ty, int i) { return BM == 128 ? (i >> 2) * 64 + ty * 4 + (i & 3) : ty * 8 + i; }
     __device__ static int col(int tx, int j) { return TN == 8 ? (j >> 2) * 64 + tx * 4 + (j & 3) : tx * 4 + j; }
@@ -156,11 +163,11 @@ __global__ void __launch_bounds__(THREADS, 2)
     a.nk = b.nk = red;
     const int slices = (red + BK - 1) / BK;
     const int s0 = (int)((long long)slices * part / split), s1 = (int)((long long)slices * (part + 1) / split);
-    float acc[T::TM][T::TN];
+    float2 acc[T::AM][T::AN];
 #pragma unroll
-    for (int i = 0; i < T::TM; ++i)
+    for (int i = 0; i < T::AM; ++i)
 #pragma unroll
-        for (int j = 0; j < T::TN; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < T::AN; ++j) acc[i][j] = make_float2(0.f, 0.f);
     const int group = threadIdx.x / T::LANES, lane = threadIdx.x % T::LANES;
     const int tx = lane % (BN / T::TN), ty = lane / (BN / T::TN);
     if (s0 < s1) {
@@ -181,7 +188,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
         for (int i = 0; i < BK / T::G; ++i) {
             const int c = group * (BK / T::G) + i;
-            float av[T::TM], bv[T::TN];
+            __align__(16) float av[T::TM], bv[T::TN];
 #pragma unroll
             for (int h = 0; h < T::TM; h += 4)
                 *reinterpret_cast<float4*>(av + h) =
@@ -191,11 +198,30 @@ __global__ void __launch_bounds__(THREADS, 2)
                 *reinterpret_cast<float4*>(bv + h) =
                     *reinterpret_cast<const float4*>(Bs + c * T::BPITCH + b.at(T::col(tx, h), c));
 #pragma unroll
-            for (int m = 0; m < T::TM; ++m)
+            for (int m = 0; m < T::AM; ++m)
 #pragma unroll
-                for (int n = 0; n < T::TN; ++n) acc[m][n] = fmaf(av[m], bv[n], acc[m][n]);
+                for (int n = 0; n < T::AN; ++n) {
+                    float2 p, q;
+                    if constexpr (T::COLS) {
+                        p = make_float2(av[m], av[m]);
+                        q = make_float2(bv[2 * n], bv[2 * n + 1]);
+                    } else {
+                        p = make_float2(av[2 * m], av[2 * m + 1]);
+                        q = make_float2(bv[n], bv[n]);
+                    }
+                    acc[m][n] = ptx::fma2(p, q, acc[m][n]);
+                }
         }
     }
+    // outputs (i, j) to (i, j + 3) of the thread
+    auto sums = [&](int i, int j) {
+        if constexpr (T::COLS) {
+            return make_float4(acc[i][j / 2].x, acc[i][j / 2].y, acc[i][j / 2 + 1].x, acc[i][j / 2 + 1].y);
+        } else {
+            const float2* q = acc[i / 2] + j;
+            return i % 2 ? make_float4(q[0].y, q[1].y, q[2].y, q[3].y) : make_float4(q[0].x, q[1].x, q[2].x, q[3].x);
+        }
+    };
     if (T::G == 1 && split == 1) {
 #pragma unroll
         for (int i = 0; i < T::TM; ++i) {
@@ -204,8 +230,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             for (int j = 0; j < T::TN; j += 4) {
                 const int n = T::col(tx, j);
                 if (m < m_rows && n < n_cols)
-                    *reinterpret_cast<float4*>(dst + (size_t)m * ldc + n) =
-                        make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+                    *reinterpret_cast<float4*>(dst + (size_t)m * ldc + n) = sums(i, j);
             }
         }
         return;
@@ -217,7 +242,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
         for (int j = 0; j < T::TN; j += 4)
             *reinterpret_cast<float4*>(sm + (group * BM_ + T::row(ty, i)) * BN + T::col(tx, j)) =
-                make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+                sums(i, j);
     if (split > 1) ptx::cluster_sync();
     else __syncthreads();
     const uint32_t base = ptx::smem_addr(sm);

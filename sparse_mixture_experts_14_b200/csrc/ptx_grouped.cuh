@@ -31,6 +31,17 @@ __device__ __forceinline__ uint64_t desc_kmajor(uint32_t saddr, int row_bytes) {
     return d;
 }
 
+// Two fp32 fused multiply-adds in one instruction, each rounded as fmaf rounds.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 // 16 bytes of a cluster's shared memory.
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
     float4 v;
