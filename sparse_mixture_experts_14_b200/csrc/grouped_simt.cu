@@ -4,15 +4,15 @@
 //     dgrad  dx_r = W_e^T dy_r                   rows [M][N] -> [M][K]
 //     wgrad  dW_e = sum_{r in e} dy_r x_r^T      -> [E][N][K]
 // A block computes BM rows x 128 columns of the output over slices of BK of the
-// reduction; the next slice is read into registers while this one is multiplied.
-// BM is 128 (8 x 8 outputs a thread), or 32 or 8 where segments have few rows: there the
-// weights' bytes bound the product, as long as no more than the rows' own work is
-// done on them.  The thread groups of a low tile (8 x 4 outputs a thread) split every
-// slice, and where tiles are few, the blocks of a cluster split the reduction; their
-// sums are added through (distributed) shared memory in a fixed order.
+// reduction; the next ones are read into registers while this one is multiplied.
+// BM is 128 (8 x 8 outputs a thread), or 64, 32 or 8 (8 x 4) where segments have few rows:
+// there the weights' bytes bound the product, as long as no more than the rows' own work is
+// done on them.  The thread groups of a low tile split every slice, and where tiles are few,
+// the blocks of a cluster split the reduction; their sums are added through (distributed)
+// shared memory in a fixed order.
 //
 // Measured: 6296 rows of 7 experts, 1416 x 1264, 0.57 ms (0.67 with a product to an instruction); 1003 rows
-// of 5, 80 us; weight gradients of 8192 rows, 4 experts of 2048 x 1024, 0.72 ms (48 TFLOP/s; 0.92 with one).
+// of 5, 86 us; weight gradients of 8192 rows, 4 experts of 2048 x 1024, 0.68 ms (51 TFLOP/s; 0.92 with one).
 // What bounds it is the multiply-adds, and the last wave of blocks where it is not full.
 //
 // Operands lie in shared memory with the reduction outermost.  Those that are read along
@@ -37,14 +37,17 @@ struct Tile {
     static constexpr int LANES = (BM / TM) * (BN / TN);   // threads that cover the tile once
     static constexpr int G = THREADS / LANES;             // thread groups
     static constexpr int BK = BM == 128 ? 16 : 32;
-    static constexpr int APITCH = BM == 32 ? BM : BM + 4, BPITCH = BM == 128 ? BN + 4 : BN;
+    static constexpr int APITCH = BM == 32 || BM == 64 ? BM : BM + 4, BPITCH = BM == 128 ? BN + 4 : BN;
     static constexpr int SLICE = BK * (APITCH + BPITCH);   // floats
     static constexpr int OPERANDS = 2 * SLICE * 4;         // two slices in turn
+    // slices on their way in registers: two where the weights' bytes bound the product (dgrad, 15 rows of 8
+    // experts, 7592 x 6240: 257 -> 233 us; in tiles of 32 rows the registers are short: 478 rows of 26, 306 -> 380)
+    static constexpr int AHEAD = BM == 8 ? 2 : 1;
     static constexpr int SUMS = G * BM * BN * 4;
     static constexpr int SMEM = OPERANDS > SUMS ? OPERANDS : SUMS;
     // Two products to an instruction (fma.rn.f32x2): of neighbouring columns, or of neighbouring rows.  The
     // other factor is doubled on the way, so the fewer of those the better (200 rows of 8 experts, 4096 x 2048:
-    // 176 us in columns, 160 in rows); the high tile has as many of either and fewer registers to spare in rows
+    // 176 us in columns, 160 in rows, the reduction in as many parts); the high tile has as many of either and fewer registers to spare in rows
     // (6296 rows of 7, 1416 x 1264: 569 in columns, 610 in rows).
     static constexpr bool COLS = BM == 128;
     static constexpr int AM = COLS ? TM : TM / 2, AN = COLS ? TN / 2 : TN;   // a thread's sums, in pairs
@@ -57,14 +60,14 @@ __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpr
 
 // One operand of the tile: element (i, k), i < ni along the tile, k in [k0, nk) along the reduction, at
 // base[i * ld + k] (KMAJ) or base[k * ld + i].
-template <int ROWS, int BK, bool KMAJ>
+template <int ROWS, int BK, bool KMAJ, int AHEAD>
 struct Operand {
     static constexpr int VECS = ROWS * BK / 4;
     static constexpr int NV = (VECS + THREADS - 1) / THREADS;
     const float* base;
     size_t ld;
     int ni, nk;
-    float4 v[NV];
+    float4 v[AHEAD][NV];
     __device__ __forceinline__ void place(int j, int& i, int& k) const {
         const int x = threadIdx.x + THREADS * j;
         if (KMAJ) {
@@ -75,21 +78,22 @@ struct Operand {
             i = x % (ROWS / 4) * 4;
         }
     }
-    __device__ __forceinline__ void fetch(int k0) {
+    __device__ __forceinline__ void fetch(int k0, int d) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             int i, k;
             place(j, i, k);
             k += k0;
             const bool in = (VECS % THREADS == 0 || (int)threadIdx.x + THREADS * j < VECS) && i < ni && k < nk;
-            v[j] = in ? load4(base + (KMAJ ? (size_t)i * ld + k : (size_t)k * ld + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[d][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (in) v[d][j] = load4(base + (KMAJ ? (size_t)i * ld + k : (size_t)k * ld + i));
         }
     }
     // position of column i in row k
     static __device__ __forceinline__ int at(int i, int k) {
         return BK == 32 && ROWS >= 32 ? i ^ ((k >> 2) % (BK / 4) * 4) : i;
     }
-    __device__ __forceinline__ void put(float* s, int pitch) const {
+    __device__ __forceinline__ void put(float* s, int pitch, int d) const {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             if (VECS % THREADS != 0 && (int)threadIdx.x + THREADS * j >= VECS) continue;
@@ -97,12 +101,12 @@ struct Operand {
             place(j, i, k);
             if (KMAJ) {
                 float* p = s + k * pitch + at(i, k);   // (k is a multiple of 4: one permutation for all four)
-                p[0] = v[j].x;
-                p[pitch] = v[j].y;
-                p[2 * pitch] = v[j].z;
-                p[3 * pitch] = v[j].w;
+                p[0] = v[d][j].x;
+                p[pitch] = v[d][j].y;
+                p[2 * pitch] = v[d][j].z;
+                p[3 * pitch] = v[d][j].w;
             } else {
-                *reinterpret_cast<float4*>(s + k * pitch + at(i, k)) = v[j];
+                *reinterpret_cast<float4*>(s + k * pitch + at(i, k)) = v[d][j];
             }
         }
     }
@@ -121,8 +125,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (threadIdx.x < 32) build_segments(&tab, seg, BM_, blockIdx.x == 0 ? status : nullptr);
     __syncthreads();
     const int part = blockIdx.x % split, tile = blockIdx.x / split;   // CTA of the cluster, cluster
-    Operand<BM_, BK, OP != kGroupedWgrad> a;
-    Operand<BN, BK, OP == kGroupedMm> b;
+    Operand<BM_, BK, OP != kGroupedWgrad, T::AHEAD> a;
+    Operand<BN, BK, OP == kGroupedMm, T::AHEAD> b;
     int red, m_rows, n_cols;   // reduction, rows and columns of the tile that exist
     float* dst;
     size_t ldc;
@@ -170,47 +174,54 @@ __global__ void __launch_bounds__(THREADS, 2)
         for (int j = 0; j < T::AN; ++j) acc[i][j] = make_float2(0.f, 0.f);
     const int group = threadIdx.x / T::LANES, lane = threadIdx.x % T::LANES;
     const int tx = lane % (BN / T::TN), ty = lane / (BN / T::TN);
-    if (s0 < s1) {
-        a.fetch(s0 * BK);
-        b.fetch(s0 * BK);
-    }
-    for (int s = s0; s < s1; ++s) {
-        // (the slice before the last was read by everyone before the barrier of the last one)
-        float* As = sm + (s & 1) * T::SLICE;
-        float* Bs = As + BK * T::APITCH;
-        a.put(As, T::APITCH);
-        b.put(Bs, T::BPITCH);
-        __syncthreads();
-        if (s + 1 < s1) {
-            a.fetch((s + 1) * BK);
-            b.fetch((s + 1) * BK);
+#pragma unroll
+    for (int d = 0; d < T::AHEAD; ++d)
+        if (s0 + d < s1) {
+            a.fetch((s0 + d) * BK, d);
+            b.fetch((s0 + d) * BK, d);
         }
+    for (int t = s0; t < s1; t += T::AHEAD) {
 #pragma unroll
-        for (int i = 0; i < BK / T::G; ++i) {
-            const int c = group * (BK / T::G) + i;
-            __align__(16) float av[T::TM], bv[T::TN];
+        for (int d = 0; d < T::AHEAD; ++d) {
+            const int s = t + d;
+            if (s >= s1) break;
+            // (the slice before the last was read by everyone before the barrier of the last one)
+            float* As = sm + (s & 1) * T::SLICE;
+            float* Bs = As + BK * T::APITCH;
+            a.put(As, T::APITCH, d);
+            b.put(Bs, T::BPITCH, d);
+            __syncthreads();
+            if (s + T::AHEAD < s1) {
+                a.fetch((s + T::AHEAD) * BK, d);
+                b.fetch((s + T::AHEAD) * BK, d);
+            }
 #pragma unroll
-            for (int h = 0; h < T::TM; h += 4)
-                *reinterpret_cast<float4*>(av + h) =
-                    *reinterpret_cast<const float4*>(As + c * T::APITCH + a.at(T::row(ty, h), c));
+            for (int i = 0; i < BK / T::G; ++i) {
+                const int c = group * (BK / T::G) + i;
+                __align__(16) float av[T::TM], bv[T::TN];
 #pragma unroll
-            for (int h = 0; h < T::TN; h += 4)
-                *reinterpret_cast<float4*>(bv + h) =
-                    *reinterpret_cast<const float4*>(Bs + c * T::BPITCH + b.at(T::col(tx, h), c));
+                for (int h = 0; h < T::TM; h += 4)
+                    *reinterpret_cast<float4*>(av + h) =
+                        *reinterpret_cast<const float4*>(As + c * T::APITCH + a.at(T::row(ty, h), c));
 #pragma unroll
-            for (int m = 0; m < T::AM; ++m)
+                for (int h = 0; h < T::TN; h += 4)
+                    *reinterpret_cast<float4*>(bv + h) =
+                        *reinterpret_cast<const float4*>(Bs + c * T::BPITCH + b.at(T::col(tx, h), c));
 #pragma unroll
-                for (int n = 0; n < T::AN; ++n) {
-                    float2 p, q;
-                    if constexpr (T::COLS) {
-                        p = make_float2(av[m], av[m]);
-                        q = make_float2(bv[2 * n], bv[2 * n + 1]);
-                    } else {
-                        p = make_float2(av[2 * m], av[2 * m + 1]);
-                        q = make_float2(bv[n], bv[n]);
+                for (int m = 0; m < T::AM; ++m)
+#pragma unroll
+                    for (int n = 0; n < T::AN; ++n) {
+                        float2 p, q;
+                        if constexpr (T::COLS) {
+                            p = make_float2(av[m], av[m]);
+                            q = make_float2(bv[2 * n], bv[2 * n + 1]);
+                        } else {
+                            p = make_float2(av[2 * m], av[2 * m + 1]);
+                            q = make_float2(bv[n], bv[n]);
+                        }
+                        acc[m][n] = ptx::fma2(p, q, acc[m][n]);
                     }
-                    acc[m][n] = ptx::fma2(p, q, acc[m][n]);
-                }
+            }
         }
     }
     // outputs (i, j) to (i, j + 3) of the thread
@@ -282,23 +293,31 @@ cudaError_t launch(const GroupedArgs& a, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
     const int M = a.seg.M, E = a.seg.E, sms = a.num_sms > 0 ? a.num_sms : 148;
-    long long tiles;
+    long long tiles;   // at most
+    float likely;      // tiles
     int red;
     if (OP == kGroupedWgrad) {
         tiles = (long long)E * ((a.N + BM - 1) / BM) * ((a.K + BN - 1) / BN);
+        likely = (float)tiles;
         red = M / E;   // on average
     } else {
-        const int ncol = OP == kGroupedMm ? a.N : a.K;
+        const int ncol = OP == kGroupedMm ? a.N : a.K, cols = (ncol + BN - 1) / BN;
         red = OP == kGroupedMm ? a.K : a.N;
         const long long t = (long long)M / BM + E;
-        tiles = (t < M ? t : M) * ((ncol + BN - 1) / BN);
+        tiles = (t < M ? t : M) * cols;
+        // half a tile of every segment is empty; with counts M is a capacity: a dispatch rounds segments up to
+        // 128 rows, half of them empty again
+        const float live = a.seg.counts ? fmaxf((float)M - 64.f * E, 0.f) : (float)M;
+        likely = (live / BM + 0.5f * E) * cols;
     }
-    // the split whose waves of blocks (two to an SM) do the least work each, a little more for every further
-    // part; eight slices a part at least
+    // Parts of the reduction: the time of a part (its slices, one to fill the pipe and half of one for each of
+    // the sums to add) times the parts that an SM gets, the last wave half full.  (8192 rows of 4 experts, weight
+    // gradients of 2048 x 1024, in 1, 2, 4, 8 parts: 791, 676, 725, 801 us; 645 rows of 8, 720 x 2072: 287, 152,
+    // 125, 113.)  Eight slices a part at least.
     int split = 1;
     float best = 1e30f;
     for (int s = 1; s <= MAX_SPLIT && (s == 1 || red >= 8 * T::BK * s); s *= 2) {
-        const float cost = (float)((tiles * s + 2 * sms - 1) / (2 * sms)) / s * (1.f + 0.03f * s);
+        const float cost = (likely * s / sms + 0.5f) * ((float)red / (T::BK * s) + 1.f + 0.5f * s);
         if (cost < best) {
             best = cost;
             split = s;
@@ -331,7 +350,10 @@ cudaError_t launch_op(const GroupedArgs& a, cudaStream_t s) {
     const int rows = OP == kGroupedWgrad ? a.N : (a.seg.M + a.seg.E - 1) / a.seg.E;
     if (rows <= 8) return launch<OP, 8>(a, s);
     // (with counts M is a capacity: a dispatch gives every expert 128 rows and room for 127 more)
-    if (rows <= 48 || (OP != kGroupedWgrad && a.seg.counts && rows <= 144)) return launch<OP, 32>(a, s);
+    if (rows <= 40 || (OP != kGroupedWgrad && a.seg.counts && rows <= 144)) return launch<OP, 32>(a, s);
+    // (8 experts of 4096 x 2048: tiles of 32, 64 and 128 rows take 137, 252 and 412 us where each expert has one;
+    // segments differ in length, so a height is taken up to about its own)
+    if (rows <= 64) return launch<OP, 64>(a, s);
     return launch<OP, 128>(a, s);
 }
 

@@ -108,6 +108,22 @@ def test_smallest_steps_fp32(moe, op, size, seg):
 
 
 @pytest.mark.parametrize("op", ["mm", "dgrad", "wgrad"])
+@pytest.mark.parametrize("counts", [[50, 51, 0, 99, 64, 40], [64], [1, 127], [66, 41, 88], [8, 40, 30]], ids=str)
+@pytest.mark.parametrize("size", [(60, 2052), (1100, 60), (64, 64), (44, 396)], ids=str)
+def test_middling_segments_fp32(moe, op, counts, size):
+    """Rows (for the weight gradient: features) between the heights of two tiles, with and without the
+    reduction split."""
+    starts, rows = segments(counts, 1, 2, 3)
+    off, cnt = device_segments(counts, starts, rows, False)
+    gen = torch.Generator(device="cuda").manual_seed(24)
+    x, dy = randn(gen, (rows, size[1]), 1.0, DT["f32"]), randn(gen, (rows, size[0]), 0.5, DT["f32"])
+    W = randn(gen, (len(counts), *size), size[1] ** -0.5, DT["f32"])
+    out = _run(moe, op, x, dy, W, off, cnt, _out(op, rows, len(counts), *size, "f32"))
+    assert moe.moe_get_device_status() == moe.MOE_OK
+    _verify(op, out, counts, starts, x, dy, W)
+
+
+@pytest.mark.parametrize("op", ["mm", "dgrad", "wgrad"])
 @pytest.mark.parametrize("counts", [[1500, 0, 2600, 900], [9, 8, 0, 7], [60, 200, 2, 90]], ids=str)
 @pytest.mark.parametrize("N,K", [(2056, 1736), (5120, 640), (1024, 4608)], ids=str)
 @pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
