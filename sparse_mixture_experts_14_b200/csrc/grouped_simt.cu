@@ -47,7 +47,7 @@ struct Tile {
     static constexpr int SMEM = OPERANDS > SUMS ? OPERANDS : SUMS;
     // Two products to an instruction (fma.rn.f32x2): of neighbouring columns, or of neighbouring rows.  The
     // other factor is doubled on the way, so the fewer of those the better (200 rows of 8 experts, 4096 x 2048:
-    // 176 us in columns, 160 in rows, the reduction in as many parts); the high tile has as many of either and fewer registers to spare in rows
+    // 176 us in columns, 160 in rows); the high tile has as many of either and fewer registers to spare in rows
     // (6296 rows of 7, 1416 x 1264: 569 in columns, 610 in rows).
     static constexpr bool COLS = BM == 128;
     static constexpr int AM = COLS ? TM : TM / 2, AN = COLS ? TN / 2 : TN;   // a thread's sums, in pairs
