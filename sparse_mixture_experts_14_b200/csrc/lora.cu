@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(THREADS) lora_shrink_kernel(const ShrinkParams
                            live ? src[j] + (size_t)kb * KC : p.x, live);
             }
         };
+        // (the tensor cores truncate when they add: 64 of the reduction in them, the rest with rounding)
         float acc[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -181,6 +182,7 @@ __global__ void __launch_bounds__(THREADS) lora_shrink_kernel(const ShrinkParams
             if (kb + NST - 1 < kb1) load(kb + NST - 1);
             asm volatile("cp.async.commit_group;" ::: "memory");
             const uint32_t sx = ring0 + (uint32_t)((kb - kb0) % NST) * STAGE_BYTES, sa = sx + TILE_BYTES;
+            float d[4][4] = {};
 #pragma unroll
             for (int kk = 0; kk < KC / 16; ++kk) {
                 uint32_t a[4], b[2][4];
@@ -192,8 +194,12 @@ __global__ void __launch_bounds__(THREADS) lora_shrink_kernel(const ShrinkParams
                     ldmatrix4(b[j], sa + br * 128 + ((bc ^ (br & 7)) * 16));
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mma16816(acc[i], a, b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
+                for (int i = 0; i < 4; ++i) mma16816(d[i], a, b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] += d[i][j];
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
