@@ -12,7 +12,7 @@
 // shared memory in a fixed order.
 //
 // Measured: 6296 rows of 7 experts, 1416 x 1264, 0.57 ms (0.67 with a product to an instruction); 1003 rows
-// of 5, 86 us; weight gradients of 8192 rows, 4 experts of 2048 x 1024, 0.68 ms (51 TFLOP/s; 0.92 with one).
+// of 5, 79 us; weight gradients of 8192 rows, 4 experts of 2048 x 1024, 0.68 ms (51 TFLOP/s; 0.92 with one).
 // What bounds it is the multiply-adds, and the last wave of blocks where it is not full.
 //
 // Operands lie in shared memory with the reduction outermost.  Those that are read along
