@@ -27,6 +27,7 @@ struct SegTable {
     int rows[kMaxGroups];
     int base[kMaxGroups + 1];
     int total;
+    bool good;   // (a table of which no segment has rows may be good or bad)
 };
 
 // Built by one whole warp.  A segment outside the row buffers, or one that runs
@@ -61,6 +62,7 @@ __device__ __forceinline__ void build_segments(SegTable* t, const Segments& s, i
         if (!ok) record_status(status, MOE_ERR_DEVICE);
         t->base[s.E] = carry;
         t->total = ok ? carry : 0;
+        t->good = ok;
     }
     if (!ok) {
         __syncwarp();

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     float* dst;
     size_t ldc;
     if (OP == kGroupedWgrad) {
-        if (tab.total != tab.base[seg.E]) return;   // bad segments: nothing is written
+        if (!tab.good) return;   // bad segments: nothing is written
         const int tk = (K + BN - 1) / BN, tn = (N + BM_ - 1) / BM_;
         const int e = tile / (tk * tn), n0 = tile / tk % tn * BM_, k0 = tile % tk * BN;
         red = tab.rows[e];

@@ -266,8 +266,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
         __syncwarp();
         if (lane == 0) {
             const int nf = (p.F + CF::PAIR_F - 1) / CF::PAIR_F;
-            const bool ok = ctrl->seg.total == ctrl->seg.base[p.seg.E];
-            ctrl->total = !ok ? 0 : WGRAD ? p.seg.E * nf * ((p.C + BN - 1) / BN) : ctrl->seg.total * nf;
+            ctrl->total = !ctrl->seg.good ? 0 : WGRAD ? p.seg.E * nf * ((p.C + BN - 1) / BN) : ctrl->seg.total * nf;
         }
     }
     ptx::tc_fence_before_sync();
