@@ -140,6 +140,35 @@ struct LoraView {
     int box;                       // ranks of a box of B: the widest of 64, 32, 16 that divides R16
 };
 
+// One output's own adapter term, u_r B^T[f], for adapter-expert pair ae; N features.
+template <int TERMS>
+__device__ __forceinline__ float adapter_term(const LoraView& l, size_t ae, int N, size_t row, int f) {
+    const uint4* bl = reinterpret_cast<const uint4*>(l.B + (ae * N + f) * l.R);
+    const uint4* ul = reinterpret_cast<const uint4*>(l.u + row * TERMS * l.R16);
+    float d = 0.f;
+#pragma unroll 2
+    for (int j = 0; j < l.R / 8; ++j) {
+        const uint4 m = __ldg(bl + j);
+        const uint32_t mw[4] = {m.x, m.y, m.z, m.w};
+        uint4 n[TERMS];
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) n[t] = ul[t * (l.R16 / 8) + j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float lo = 0.f, hi = 0.f;
+#pragma unroll
+            for (int t = TERMS - 1; t >= 0; --t) {   // (exact)
+                const uint32_t nw = i == 0 ? n[t].x : i == 1 ? n[t].y : i == 2 ? n[t].z : n[t].w;
+                lo += bf16_lo(nw);
+                hi += bf16_hi(nw);
+            }
+            d = fmaf(bf16_lo(mw[i]), lo, d);
+            d = fmaf(bf16_hi(mw[i]), hi, d);
+        }
+    }
+    return d;
+}
+
 inline size_t lora_tiles(int M, int E) { return (size_t)M / kColumnTile + E; }
 inline size_t lora_u_bytes(int M, int R) { return align_up((size_t)M * 3 * ((R + 15) / 16 * 16) * 2, 256); }
 inline size_t lora_workspace_bytes(int M, int E, int R) {

@@ -18,6 +18,7 @@
 // Only there does the block wait for the kernel that makes u: the weights stream
 // while that one runs.
 #include "grouped.cuh"
+#include "ptx_grouped.cuh"
 
 namespace moe {
 namespace {
@@ -35,15 +36,6 @@ struct FewParams {
     LoraView lora;
     int* status;
 };
-
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // Weights are read once: past L1.
 __device__ __forceinline__ uint4 load_stream(const __nv_bfloat16* p) {
@@ -145,8 +137,10 @@ __global__ void __launch_bounds__(32 * WARPS, 2) grouped_few_kernel(const FewPar
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    mma16816(part[i][t], a[u][i][0].x, a[u][i][1].x, a[u][i][0].y, a[u][i][1].y, b[u][t].x, b[u][t].y);
-                    mma16816(part[i][t], a[u][i][0].z, a[u][i][1].z, a[u][i][0].w, a[u][i][1].w, b[u][t].z, b[u][t].w);
+                    ptx::mma16816(part[i][t], a[u][i][0].x, a[u][i][1].x, a[u][i][0].y, a[u][i][1].y, b[u][t].x,
+                                  b[u][t].y);
+                    ptx::mma16816(part[i][t], a[u][i][0].z, a[u][i][1].z, a[u][i][0].w, a[u][i][1].w, b[u][t].z,
+                                  b[u][t].w);
                 }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -172,33 +166,7 @@ __global__ void __launch_bounds__(32 * WARPS, 2) grouped_few_kernel(const FewPar
         for (int v = 0; v < WARPS; ++v) s += red[v][r][fl];
         if (LORA) {
             const int id = p.lora.adapter[row0 + r];
-            if (id >= 0 && id < p.lora.L) {
-                const uint4* bl = reinterpret_cast<const uint4*>(
-                    p.lora.B + (((size_t)id * p.seg.E + e) * N + f) * p.lora.R);
-                const uint4* ul = reinterpret_cast<const uint4*>(p.lora.u + (row0 + r) * TERMS * p.lora.R16);
-                float d = 0.f;
-#pragma unroll 2
-                for (int j = 0; j < p.lora.R / 8; ++j) {
-                    const uint4 m = __ldg(bl + j);
-                    const uint32_t mw[4] = {m.x, m.y, m.z, m.w};
-                    uint4 n[TERMS];
-#pragma unroll
-                    for (int t = 0; t < TERMS; ++t) n[t] = ul[t * (p.lora.R16 / 8) + j];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float lo = 0.f, hi = 0.f;
-#pragma unroll
-                        for (int t = TERMS - 1; t >= 0; --t) {   // (exact)
-                            const uint32_t nw = i == 0 ? n[t].x : i == 1 ? n[t].y : i == 2 ? n[t].z : n[t].w;
-                            lo += bf16_lo(nw);
-                            hi += bf16_hi(nw);
-                        }
-                        d = fmaf(bf16_lo(mw[i]), lo, d);
-                        d = fmaf(bf16_hi(mw[i]), hi, d);
-                    }
-                }
-                s += d;
-            }
+            if (id >= 0 && id < p.lora.L) s += adapter_term<TERMS>(p.lora, (size_t)id * p.seg.E + e, N, row0 + r, f);
         }
         const size_t at = (row0 + r) * N + f;
         if (OUT16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(s);

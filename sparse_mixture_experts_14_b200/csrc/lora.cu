@@ -58,14 +58,6 @@ struct ShrinkSmem {
 constexpr int SMEM_BYTES = NST * STAGE_BYTES;   // also holds the partial sums of a pass
 static_assert(WIN * PITCH * 4 <= SMEM_BYTES, "partial sums");
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -194,7 +186,8 @@ __global__ void __launch_bounds__(THREADS) lora_shrink_kernel(const ShrinkParams
                     ldmatrix4(b[j], sa + br * 128 + ((bc ^ (br & 7)) * 16));
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mma16816(d[i], a, b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
+                for (int i = 0; i < 4; ++i)
+                    ptx::mma16816(d[i], a[0], a[1], a[2], a[3], b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
