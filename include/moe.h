@@ -567,7 +567,8 @@ MOE_API moe_status moe_grouped_wgrad(const void* dy, const void* x, const int32_
  * With a bfloat16 output s_a A x is rounded once to bf16 (the second product's
  * operand type), with a float output it keeps fp32's digits; the sum of both
  * products is rounded once.  A NaN or Inf in an adapter reaches the
- * rows of that adapter only (other rows may be summed in another order then).
+ * rows of that adapter only (other rows may be summed in another order then,
+ * and the call takes several times as long).
  * An id outside [-1, L) in a segment records
  * MOE_ERR_DEVICE.  Sizes: as moe_grouped_mm; R a multiple of 8, at most
  * MOE_LORA_MAX_RANK.  workspace: moe_grouped_lora_workspace_size() bytes

@@ -38,8 +38,9 @@
 // the tile's rows of u with zeros in the rows of other adapters (B side): one K = 16
 // MMA a slice, four slices a stage.  Boxes are 64, 32 or 16 ranks wide, the widest
 // that divides the padded rank, with the swizzle of that width.  A zero does not
-// hide an infinity or NaN in another request's adapter, so where the sum is not finite
-// the epilogue computes that output again from its own terms alone.
+// hide an infinity or NaN in another request's adapter: it takes that feature of all of the
+// tile's rows with it.  The epilogue marks such tiles, and behind the pipeline, where no
+// bounded wait depends on it, the CTA computes those outputs again from their own terms.
 //
 // Outputs of few tiles: a cluster of up to 4 pairs splits a tile's reduction (SPLIT).
 // Every pair keeps its fp32 sums in shared memory, and the CTAs add them through
@@ -103,6 +104,7 @@ struct Params {
 
 constexpr int MAX_STAGES = 6;
 constexpr int MAX_SPLIT = 4;                // pairs of a cluster
+constexpr int ODD_WORDS = 8;                // tiles 256 apart share a bit: a tile may be looked through in vain
 
 struct Ctrl {
     uint64_t full[MAX_STAGES];     // leader: both CTAs' bytes of a stage landed
@@ -115,6 +117,7 @@ struct Ctrl {
     uint32_t tmem_base;
     int abort;
     int total;
+    uint32_t odd[ODD_WORDS];   // adapters: this CTA's tiles with features of which no output is finite, in turn
     SegTable seg;
 };
 
@@ -182,6 +185,13 @@ __device__ __forceinline__ Tile decode(const Ctrl* c, const Params& p, int tile)
     return t;
 }
 
+// Pairs of bf16 values: the smaller magnitudes; NaN only where both are.
+__device__ __forceinline__ uint32_t min_magnitude(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                     __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+
 // Index of the row box that holds n rows (n a multiple of 16, at most 128).
 __device__ __forceinline__ int box_of(int n) { return n <= 16 ? 0 : n <= 32 ? 1 : n <= 64 ? 2 : 3; }
 
@@ -193,32 +203,90 @@ __device__ __forceinline__ int tile_slices(const LoraView& l, int col_tile) {
 // What the TMA's swizzle of rows of 2 box bytes does to row r: its 16-byte chunk c is kept at c ^ swizzle.
 __device__ __forceinline__ int swizzle(int r, int box) { return box == 64 ? r & 7 : box == 32 ? r >> 1 & 3 : r >> 2 & 1; }
 
-// One output from its own terms: x_r W_e^T[f] and, with an adapter, u_r B_{a,e}^T[f].
-__device__ __forceinline__ float recompute(const Params& p, int e, size_t r, int f) {
-    const __nv_bfloat16* w = p.W + ((size_t)e * p.F + f) * p.red;
-    const __nv_bfloat16* x = p.x + r * p.red;
-    float s = 0.f;
-#pragma unroll 1
-    for (int k = 0; k < p.red; k += 2) {
-        const uint32_t a = *reinterpret_cast<const uint32_t*>(x + k), b = *reinterpret_cast<const uint32_t*>(w + k);
-        s = fmaf(bf16_lo(a), bf16_lo(b), s);
-        s = fmaf(bf16_hi(a), bf16_hi(b), s);
+__device__ __forceinline__ bool not_finite(uint32_t bits) { return (bits & 0x7f800000u) == 0x7f800000u; }
+
+// Outputs of a tile with adapters that are not finite, again from their own terms alone: x_r W_e^T[f] and, with an
+// adapter, u_r B_{a,e}^T[f].  One warp, the 16 features from f0 on and n <= 32 rows, row0 and every step-th behind.
+// What another request's B does to a feature (zero times an infinity or NaN) it does to all of the tile's rows, so
+// a block in which every feature has a finite output is left as it is.  Products as in grouped_few.cu, operands
+// straight from global memory, 32 of the reduction in the tensor cores at a time and the rest with rounding.
+// (All outputs hit: 1500 rows of one expert,
+// 2048 x 2048, 43 -> 314 us; 4096 rows of 8, 14336 x 4096, 0.46 -> 5.3 ms, bound by L2.  One lane an output took 32 ms
+// for the first, inside the pipeline, whose waits are bounded.)
+__device__ __noinline__ void repair(const Params& p, int e, size_t row0, int n, int step, int f0) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int F = p.F, K = p.red;
+    // this lane's outputs: features f0 + 8 j + g, rows 8 t + 2 q + i
+    uint32_t bad = 0;   // bit 8 j + 2 t + i
+    bool all[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int f = f0 + 8 * j + g;
+        all[j] = f < F;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int r = 8 * (c >> 1) + 2 * q + (c & 1);
+            if (f >= F || r >= n) continue;
+            const size_t at = (row0 + (size_t)r * step) * F + f;
+            const uint32_t bits = p.out16 ? (uint32_t)static_cast<const uint16_t*>(p.out)[at] << 16
+                                          : static_cast<const uint32_t*>(p.out)[at];
+            if (not_finite(bits)) bad |= 1u << (8 * j + c);
+            else all[j] = false;
+        }
+        // (the lanes of a feature: four neighbours)
+        const uint32_t b = __ballot_sync(0xffffffffu, all[j]);
+        all[j] = (b >> (4 * g) & 15u) == 15u;
     }
-    const int id = p.lora.adapter[r];
-    if (id >= 0 && id < p.lora.L) {
-        const __nv_bfloat16* u = p.lora.u + r * p.lora.terms * p.lora.R16;
-        const __nv_bfloat16* b = p.lora.B + (((size_t)id * p.seg.E + e) * p.F + f) * p.lora.R;
+    if (!__any_sync(0xffffffffu, all[0] || all[1])) return;
+
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const __nv_bfloat16* w[2];
+    const __nv_bfloat16* x[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int f = f0 + 8 * j + g;
+        w[j] = p.W + ((size_t)e * F + (f < F ? f : f0)) * K + 8 * q;
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int r = 8 * t + g;
+        x[t] = p.x + (row0 + (size_t)(r < n ? r : 0) * step) * K + 8 * q;
+    }
+    float acc[4][4] = {};
 #pragma unroll 1
-        for (int j = 0; j < p.lora.R; ++j) {
-            float v = 0.f;
-            for (int t = p.lora.terms - 1; t >= 0; --t) v += __bfloat162float(u[t * p.lora.R16 + j]);
-            s = fmaf(v, __bfloat162float(b[j]), s);
+    for (int k0 = 0; k0 < K; k0 += 32) {
+        const bool in = k0 + 8 * q < K;
+        uint4 a[2], b[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) a[j] = in ? __ldg(reinterpret_cast<const uint4*>(w[j] + k0)) : zero;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) b[t] = in ? __ldg(reinterpret_cast<const uint4*>(x[t] + k0)) : zero;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            float d[4] = {};
+            ptx::mma16816(d, a[0].x, a[1].x, a[0].y, a[1].y, b[t].x, b[t].y);
+            ptx::mma16816(d, a[0].z, a[1].z, a[0].w, a[1].w, b[t].z, b[t].w);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[t][c] += d[c];
         }
     }
-    return s;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            if (!(bad >> (8 * j + c) & 1)) continue;
+            const int f = f0 + 8 * j + g;
+            const size_t r = row0 + (size_t)(8 * (c >> 1) + 2 * q + (c & 1)) * step;
+            float s = acc[c >> 1][2 * j + (c & 1)];
+            const int id = p.lora.adapter[r];
+            if (id >= 0 && id < p.lora.L) {
+                const size_t ae = (size_t)id * p.seg.E + e;
+                s += p.lora.terms == 1 ? adapter_term<1>(p.lora, ae, F, r, f) : adapter_term<3>(p.lora, ae, F, r, f);
+            }
+            if (p.out16) static_cast<__nv_bfloat16*>(p.out)[r * F + f] = __float2bfloat16_rn(s);
+            else static_cast<float*>(p.out)[r * F + f] = s;
+        }
 }
-
-__device__ __forceinline__ bool not_finite(uint32_t bits) { return (bits & 0x7f800000u) == 0x7f800000u; }
 
 template <int OP, bool OUT16, int W, bool LORA, bool SPLIT>
 __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
@@ -256,6 +324,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
         ptx::fence_mbar_init();
         ptx::tma_prefetch_desc(&maps.a);
     }
+    if (LORA && threadIdx.x >= 32 && threadIdx.x < 32 + ODD_WORDS) ctrl->odd[threadIdx.x - 32] = 0;
     if (warp == 1) {
         ptx::tmem_alloc_pair(&ctrl->tmem_base, TMEM_COLS);
         ptx::tmem_relinquish_pair();
@@ -289,6 +358,10 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                      min((max(b1 - t.nkb, 0) + 1) / 2 * SLICES, slices)};
     };
     const ptx::WaitCtl wc{&ctrl->abort, p.status, (uint64_t)p.wait_ns};
+    auto mark_odd = [&](int tile) {   // one lane
+        const int i = SPLIT ? 0 : (tile - cluster) / nclusters;
+        atomicOr(&ctrl->odd[i / 32 % ODD_WORDS], 1u << i % 32);
+    };
 
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer (both CTAs)
@@ -574,15 +647,14 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                 const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
                 const int aslices = LORA ? tile_slices(p.lora, t.col_tile) : 0;
                 const size_t row0 = (WGRAD ? (size_t)t.e * p.C : (size_t)0) + t.c0 + c0;
-                bool odd = false;   // something is not finite: zero times a finite value is zero
-                if (LORA && aslices > 0) {
-                    __nv_bfloat162 t2 = __floats2bfloat162_rn(0.f, 0.f);
-                    const __nv_bfloat162 zero = t2;
+                if (LORA && aslices > 0 && ncol > 0) {
+                    // the smallest magnitude of the lane's feature, NaN aside: infinite (or NaN) if none is finite
+                    uint32_t least = 0x7f807f80u;
 #pragma unroll
                     for (int i = 0; i < CF::COLS; i += 2)
-                        if (i < ncol) t2 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v[i / 2]), zero, t2);
-                    odd = !(__low2float(t2) == 0.f && __high2float(t2) == 0.f);
-                    odd = __any_sync(0xffffffffu, odd);
+                        if (i < ncol) least = min_magnitude(least, v[i / 2]);
+                    const bool odd = not_finite(least << 16) && not_finite(least);
+                    if (__any_sync(0xffffffffu, odd) && lane == 0) mark_odd(tile);
                 }
                 // Neighbouring lanes swap halves: of columns i and i + 1 the even lane stores features f, f + 1 of
                 // the first, the odd one f - 1, f of the second.  F is a multiple of 8: pairs are whole.
@@ -602,20 +674,6 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                     }
                     out += 16 * (size_t)p.F;
                     asm volatile("" : "+l"(out));   // one pointer, not one per column, in registers
-                }
-                if (LORA && odd) {
-                    // every lane goes through what it has just stored
-                    out = static_cast<__nv_bfloat16*>(p.out) + (row0 + hi) * p.F + fp;
-#pragma unroll 1
-                    for (int i = 0; i < min(cols, ncol); i += 2) {
-#pragma unroll 1
-                        for (int j = 0; j < 2; ++j) {
-                            const uint32_t bits = (uint32_t)__bfloat16_as_ushort(out[(size_t)i * p.F + j]) << 16;
-                            if (not_finite(bits))
-                                out[(size_t)i * p.F + j] = __float2bfloat16_rn(recompute(p, t.e, row0 + hi + i, fp + j));
-                        }
-                    }
-                    __syncwarp();
                 }
             } else {
                 float sum[CF::COLS];
@@ -671,18 +729,12 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                     out += 16 * (size_t)p.F;
                     asm volatile("" : "+l"(out));
                 }
-                if (LORA && aslices > 0) {
-                    float z = 0.f;   // (zero times a finite value is zero)
+                if (LORA && aslices > 0 && ncol > 0) {
+                    float least = __uint_as_float(0x7f800000u);
 #pragma unroll
-                    for (int i = 0; i < CF::COLS; ++i) z = fmaf(sum[i], 0.f, z);
-                    if (z != 0.f) {
-                        out = static_cast<float*>(p.out) + row0 * p.F + f;
-#pragma unroll 1
-                        for (int i = 0; i < min(valid, ncol); ++i)
-                            if (not_finite(__float_as_uint(out[(size_t)i * p.F])))
-                                out[(size_t)i * p.F] = recompute(p, t.e, row0 + i, f);
-                    }
-                    __syncwarp();
+                    for (int i = 0; i < CF::COLS; ++i)
+                        if (i < ncol) least = fminf(least, fabsf(sum[i]));
+                    if (__any_sync(0xffffffffu, not_finite(__float_as_uint(least))) && lane == 0) mark_odd(tile);
                 }
             }
         }
@@ -806,11 +858,7 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
                         s[3] += v[i].w;
                     }
                 if (f >= p.F) continue;   // F is a multiple of 8
-                if (LORA) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (not_finite(__float_as_uint(s[j]))) s[j] = recompute(p, t.e, row0 + c, f + j);
-                }
+                if (LORA && not_finite(__float_as_uint(s[0] + s[1] + s[2] + s[3]))) mark_odd(cluster);
                 if (p.out16)
                     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + (row0 + c) * p.F + f) =
                         make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
@@ -826,6 +874,25 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
     if (warp == 1) {
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+    if (LORA) {
+        // Outputs that another request's adapter took with it, where nothing waits for this CTA any more.  Each
+        // sees to what it has stored itself.
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < ODD_WORDS; ++i) any |= ctrl->odd[i];
+        int turn = 0;
+        for (int tile = cluster; any != 0 && tile < total; tile += nclusters, ++turn) {
+            if (!(ctrl->odd[turn / 32 % ODD_WORDS] >> turn % 32 & 1)) continue;
+            const Tile t = decode<WGRAD, CF::PAIR_F>(ctrl, p, tile);
+            const int mine = SPLIT ? (t.valid - part + parts - 1) / parts : t.valid;   // rows
+            const int blocks = (mine + 31) / 32;
+            for (int i = warp; i < W * BM / 16 * blocks; i += CF::THREADS / 32) {
+                const int fg = i / blocks, c = i % blocks * 32;
+                const int f0 = t.f0 + fg / (BM / 16) * 2 * BM + (int)rank * BM + fg % (BM / 16) * 16;
+                if (f0 < p.F) repair(p, t.e, (size_t)t.c0 + part + (size_t)c * parts, min(32, mine - c), parts, f0);
+            }
+        }
     }
 }
 

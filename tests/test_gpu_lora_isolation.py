@@ -98,3 +98,20 @@ def test_a_bad_adapter_does_not_hold_up_the_batch(moe, out_dtype):
     print(f"clean {clean * 1e3:.1f} us, with an infinite adapter {slow * 1e3:.1f} us")
     assert moe.moe_get_device_status() == moe.MOE_OK
     assert slow <= 100 * clean, (clean, slow)
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+def test_long_reductions_with_a_bad_adapter(moe, out_dtype):
+    """Several tiles to a pair of CTAs, every output of each to be summed again over a reduction of 57344: no
+    bounded wait of the pipeline may run out meanwhile."""
+    counts, N, K, L, R = [2048], 4096, 57344, 5, 16
+    starts, rows, x, W, A, B, scale, ids = _inputs(counts, N, K, L, R, "runs", 73)
+    B[2] = float("inf")
+    out = _call(moe, counts, starts, rows, False, out_dtype, x, W, A, B, scale, ids)
+    assert moe.moe_get_device_status() == moe.MOE_OK
+    hit = ids == 2
+    assert not out[hit].isfinite().any()
+    clean = torch.where(hit, torch.full_like(ids, -1), ids)
+    B[2] = 0
+    out[hit] = _call(moe, counts, starts, rows, False, out_dtype, x, W, A, B, scale, clean)[hit]
+    _verify(out, counts, starts, x, W, A, B, scale, clean)
