@@ -730,6 +730,32 @@ def _grad_list(grads):
     return [g for g in grads if g is not None]
 
 
+def _grads_and_outs(grads, out):
+    """The gradients of a call and the tensor that takes each: of dicts the entry of the same name, of lists the
+    one in the same place (None beside a None gradient, or left out of a list without any)."""
+    if isinstance(out, dict):
+        if not isinstance(grads, dict):
+            raise TypeError("out must be a list beside a list of gradients: a dict is paired by name")
+        names = [n for n, g in grads.items() if g is not None and n not in ("dx", "dh")]
+        missing = [n for n in names if out.get(n) is None]
+        if missing:
+            raise ValueError(f"out has no tensor for {', '.join(missing)}")
+        return [grads[n] for n in names], [out[n] for n in names]
+    if isinstance(grads, dict):
+        grads = [g for n, g in grads.items() if n not in ("dx", "dh")]
+    grads, out = list(grads), list(out)
+    have, outs = [g for g in grads if g is not None], [o for o in out if o is not None]
+    if len(have) == len(grads) == len(out) == len(outs):
+        return grads, out
+    if len(out) == len(grads):
+        if any(o is None for g, o in zip(grads, out) if g is not None):
+            raise ValueError("out has None in the place of a gradient")
+        return have, [o for g, o in zip(grads, out) if g is not None]
+    if len(outs) != len(out) or len(out) != len(have):
+        raise ValueError(f"out has {len(out)} tensors for {len(have)} gradients")
+    return have, out
+
+
 _TENSOR_CODES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
 
 
@@ -779,17 +805,21 @@ def moe_grad_norm(grads, norm=None, stream=None):
 
 def moe_clip_grads(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
     """Scale every gradient by min(1, max_norm / (n + eps)), n the global 2-norm: in place, or into the
-    tensors of `out` (same lengths and types).  Returns (norm float32 [1], the list of clipped tensors).
+    tensors of `out` (same shapes and types; a list in the gradients' order, or for a dict of gradients a dict
+    with their names).  Returns (norm float32 [1], the list of clipped tensors).
     The dict of moe_backward_ws or moe_block_backward_ws is taken without its dx or dh.  No host
     synchronisation."""
-    grads = _grad_list(grads)
+    grads, outs = (_grad_list(grads), None) if out is None else _grads_and_outs(grads, out)
     arr, dev = _tensor_list(grads, "grads", -1)
-    outs, oarr = grads, None
-    if out is not None:
-        outs = _grad_list(out)
-        if len(outs) != len(grads):
-            raise ValueError(f"out has {len(outs)} tensors for {len(grads)} gradients")
+    oarr = None
+    if outs is None:
+        outs = grads
+    else:
         oarr, dev = _tensor_list(outs, "out", dev)   # (the library compares their lengths and types)
+        if not all(map(torch.Tensor.is_same_size, grads, outs)):
+            for i, (g, o) in enumerate(zip(grads, outs)):
+                if o.numel() == g.numel() and o.shape != g.shape:
+                    raise ValueError(f"out {i} has shape {tuple(o.shape)}, its gradient {tuple(g.shape)}")
     norm, dev = _norm_tensor(norm, dev, stream)
     _check(_lib.moe_clip_grads(arr.buffer_info()[0], oarr.buffer_info()[0] if oarr else None, len(grads), max_norm, eps,
                                _ptr(norm), _stream_on(stream, dev)), "moe_clip_grads")

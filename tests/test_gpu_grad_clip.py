@@ -238,3 +238,18 @@ def test_after_the_layers_backward(moe, dtype):
     _check_norm(norm, keep)
     _check_scaled(clipped, keep, 0.1, 1e-6)
     assert moe.moe_get_device_status() == moe.MOE_OK
+
+
+def test_outputs_by_name_and_by_shape(moe):
+    """A dict of outputs in another order than the gradients': dW1, dW3 and dW2 have one length and type."""
+    g = dict(dx=torch.ones(2, 4, device="cuda"), dWg=torch.full((2, 4), 3.0, device="cuda"),
+             dW1=torch.full((2, 6, 4), 1.0, device="cuda"), dW3=torch.full((2, 6, 4), 2.0, device="cuda"),
+             dW2=torch.full((2, 4, 6), 4.0, device="cuda"))
+    out = {n: torch.zeros_like(g[n]) for n in ("dW2", "dW3", "dW1", "dWg")}
+    norm, clipped = moe.moe_clip_grads(g, 1e9, out=out)
+    assert all(torch.equal(out[n], g[n]) for n in out)
+    assert all(a is out[n] for a, n in zip(clipped, ("dWg", "dW1", "dW3", "dW2")))
+    with pytest.raises(ValueError):
+        moe.moe_clip_grads([g["dW1"]], 1.0, out=[g["dW2"].clone()])     # one length, another shape
+    with pytest.raises(ValueError):
+        moe.moe_clip_grads(g, 1.0, out=dict(out, dW2=torch.zeros(2, 6, 4, device="cuda")))
