@@ -82,7 +82,8 @@ class SparseMoE(torch.nn.Module):
 class GroupedMmFunction(torch.autograd.Function):
     """y_r = W_e x_r for the rows of every expert's segment, with gradients for x and W.
 
-    Rows in no segment are zero in y and in the gradient of x.
+    Rows in no segment are zero in y and in the gradient of x.  The gradients are functions with gradients of
+    their own, the same three products over again, so derivatives of any order are right.
     """
 
     @staticmethod
@@ -98,10 +99,46 @@ class GroupedMmFunction(torch.autograd.Function):
         dy = dy.contiguous()
         dx = dW = None
         if ctx.needs_input_grad[0]:
-            dx = moe_grouped_dgrad(dy, W, offsets, counts, out=torch.zeros_like(x))
+            dx = GroupedDgradFunction.apply(dy, W, offsets, counts)
         if ctx.needs_input_grad[1]:
-            dW = moe_grouped_wgrad(dy, x, offsets, counts)
+            dW = GroupedWgradFunction.apply(dy, x, offsets, counts)
         return dx, dW, None, None
+
+
+class GroupedDgradFunction(torch.autograd.Function):
+    """dx_r = W_e^T dy_r for the rows of every expert's segment, zero elsewhere."""
+
+    @staticmethod
+    def forward(ctx, dy, W, offsets, counts=None):
+        dx = torch.zeros((dy.shape[0], W.shape[2]), dtype=dy.dtype, device=dy.device)
+        moe_grouped_dgrad(dy, W, offsets, counts, out=dx)
+        ctx.save_for_backward(dy, W, offsets, counts)
+        return dx
+
+    @staticmethod
+    def backward(ctx, g):
+        dy, W, offsets, counts = ctx.saved_tensors
+        g = g.contiguous()
+        ddy = GroupedMmFunction.apply(g, W, offsets, counts) if ctx.needs_input_grad[0] else None
+        dW = GroupedWgradFunction.apply(dy, g, offsets, counts) if ctx.needs_input_grad[1] else None
+        return ddy, dW, None, None
+
+
+class GroupedWgradFunction(torch.autograd.Function):
+    """dW_e = sum over segment e's rows of dy_r x_r^T."""
+
+    @staticmethod
+    def forward(ctx, dy, x, offsets, counts=None):
+        ctx.save_for_backward(dy, x, offsets, counts)
+        return moe_grouped_wgrad(dy, x, offsets, counts)
+
+    @staticmethod
+    def backward(ctx, g):
+        dy, x, offsets, counts = ctx.saved_tensors
+        g = g.contiguous()
+        ddy = GroupedMmFunction.apply(x, g, offsets, counts) if ctx.needs_input_grad[0] else None
+        dx = GroupedDgradFunction.apply(dy, g, offsets, counts) if ctx.needs_input_grad[1] else None
+        return ddy, dx, None, None
 
 
 class GroupedLinear(torch.nn.Module):

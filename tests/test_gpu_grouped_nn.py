@@ -96,3 +96,32 @@ def test_clip_grad_norm_on_the_layer(mods):
         w = k.double() * (want / 4 / (want + 1e-6))
         assert ((p.grad.double() - w).abs() <= (2.0 ** -8 + 2.0 ** -18) * w.abs()).all()
     assert nn.clip_grad_norm_([torch.nn.Parameter(torch.ones(3, device="cuda"))], 1.0).item() == 0.0
+
+
+def test_second_derivatives(mods):
+    """sum (dL/dx)^2 of L = sum y^2 / 2, by W and by x, in fp32 against the formula in 64 bits: with
+    G_e = W_e^T W_e, dL/dx_r = G_e x_r, so the penalty is sum |G x|^2."""
+    moe, nn = mods
+    counts, starts = [33, 0, 70], [0, 33, 40]
+    off = torch.tensor(starts + [110], dtype=torch.int32, device="cuda")
+    cnt = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    torch.manual_seed(7)
+    lin = nn.GroupedLinear(3, 72, 40, dtype=torch.float32)
+    x = torch.randn(110, 72, device="cuda", requires_grad=True)
+    y = lin(x, off, cnt)
+    dx, = torch.autograd.grad(y.pow(2).sum() / 2, x, create_graph=True)
+    gx, gW = torch.autograd.grad(dx.pow(2).sum(), (x, lin.W))
+    W64 = lin.W.detach().double().requires_grad_()
+    x64 = x.detach().double().requires_grad_()
+    live = torch.zeros(110, dtype=torch.bool, device="cuda")
+    pen = 0.0
+    for e, (s, n) in enumerate(zip(starts, counts)):
+        live[s:s + n] = True
+        pen = pen + (x64[s:s + n] @ W64[e].t() @ W64[e]).pow(2).sum()
+    wx, wW = torch.autograd.grad(pen, (x64, W64))
+    assert (gx[~live] == 0).all() and (gW[1] == 0).all()
+    # chains of at most five products of up to 110 terms each, every one within (n + 8) 2^-23 of its magnitudes; the
+    # magnitudes of a random chain exceed its values by sqrt(n) < 11 a product at most
+    for g, w in ((gx, wx), (gW, wW)):
+        assert (g.double() - w).abs().max() <= 5 * 118 * 2.0 ** -23 * 11 * w.abs().max()
+    assert moe.moe_get_device_status() == moe.MOE_OK
