@@ -759,16 +759,17 @@ def _grads_and_outs(grads, out):
 _TENSOR_CODES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
 
 
-def _tensor_list(tensors, name, dev):
-    """An array of moe_tensor (24 bytes each: address, length, type) and the device index of the tensors,
-    which must be `dev` unless that is -1.  One pass of C calls per property: lists are long."""
+def _tensor_list(tensors, name):
+    """An array of moe_tensor (24 bytes each: address, length, type) and the device index of the tensors (-1: there
+    are none).  One pass of C calls per property: lists are long."""
     T = torch.Tensor
     devs = set(map(T.get_device, tensors))   # (a TypeError for what is no tensor)
+    dev = -1
     if devs:
         if min(devs) < 0:
             raise TypeError(f"{name} must be CUDA tensors")
-        if len(devs | ({dev} if dev >= 0 else set())) > 1:
-            raise ValueError(f"tensors on several devices: {sorted(devs | {dev} - {-1})}")
+        if len(devs) > 1:
+            raise ValueError(f"tensors on several devices: {sorted(devs)}")
         dev = devs.pop()
     if not all(map(T.is_contiguous, tensors)):
         raise ValueError(f"{name} must be contiguous")
@@ -797,7 +798,7 @@ def moe_grad_norm(grads, norm=None, stream=None):
     """The global 2-norm of a list of gradients, bf16 and float32 mixed: float32 [1] on the device.  The dict of
     moe_backward_ws or moe_block_backward_ws is taken without its dx or dh."""
     grads = _grad_list(grads)
-    arr, dev = _tensor_list(grads, "grads", -1)
+    arr, dev = _tensor_list(grads, "grads")
     norm, dev = _norm_tensor(norm, dev, stream)
     _check(_lib.moe_grad_norm(arr.buffer_info()[0], len(grads), _ptr(norm), _stream_on(stream, dev)), "moe_grad_norm")
     return norm
@@ -809,20 +810,22 @@ def moe_clip_grads(grads, max_norm, eps=1e-6, out=None, norm=None, stream=None):
     with their names).  Returns (norm float32 [1], the list of clipped tensors).
     The dict of moe_backward_ws or moe_block_backward_ws is taken without its dx or dh.  No host
     synchronisation."""
-    grads, outs = (_grad_list(grads), None) if out is None else _grads_and_outs(grads, out)
-    arr, dev = _tensor_list(grads, "grads", -1)
-    oarr = None
-    if outs is None:
-        outs = grads
+    if out is None:
+        grads = outs = _grad_list(grads)
+        arr, dev = _tensor_list(grads, "grads")
+        gptr, optr = arr.buffer_info()[0], None
     else:
-        oarr, dev = _tensor_list(outs, "out", dev)   # (the library compares their lengths and types)
+        grads, outs = _grads_and_outs(grads, out)
+        arr, dev = _tensor_list(grads + outs, "grads and out")   # (in one list: 28 us a call of 17 tensors, 30 in two)
+        gptr = arr.buffer_info()[0]
+        optr = gptr + 24 * len(grads)
         if not all(map(torch.Tensor.is_same_size, grads, outs)):
-            for i, (g, o) in enumerate(zip(grads, outs)):
+            for i, (g, o) in enumerate(zip(grads, outs)):   # (the library compares lengths and types)
                 if o.numel() == g.numel() and o.shape != g.shape:
                     raise ValueError(f"out {i} has shape {tuple(o.shape)}, its gradient {tuple(g.shape)}")
     norm, dev = _norm_tensor(norm, dev, stream)
-    _check(_lib.moe_clip_grads(arr.buffer_info()[0], oarr.buffer_info()[0] if oarr else None, len(grads), max_norm, eps,
-                               _ptr(norm), _stream_on(stream, dev)), "moe_clip_grads")
+    _check(_lib.moe_clip_grads(gptr, optr, len(grads), max_norm, eps, _ptr(norm), _stream_on(stream, dev)),
+           "moe_clip_grads")
     return norm, outs
 
 

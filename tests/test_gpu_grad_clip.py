@@ -253,3 +253,7 @@ def test_outputs_by_name_and_by_shape(moe):
         moe.moe_clip_grads([g["dW1"]], 1.0, out=[g["dW2"].clone()])     # one length, another shape
     with pytest.raises(ValueError):
         moe.moe_clip_grads(g, 1.0, out=dict(out, dW2=torch.zeros(2, 6, 4, device="cuda")))
+    with pytest.raises(TypeError):
+        moe.moe_clip_grads([g["dW1"]], 1.0, out=[torch.zeros(2, 6, 4)])                                # on the CPU
+    with pytest.raises(moe.MoEError):
+        moe.moe_clip_grads([g["dW1"]], 1.0, out=[torch.zeros(2, 6, 4, device="cuda").bfloat16()])      # another type
