@@ -50,8 +50,23 @@ class MoEFunction(torch.autograd.Function):
         wd = torch.bfloat16 if W1.dtype == torch.bfloat16 else torch.float32
         g, _ = moe_backward_ws(x, Wg, W1, W3, W2, dout.contiguous(), ctx.k, ctx.ws, alpha=ctx.alpha, wgrad_dtype=wd)
         ctx.ws = None
-        return (g["dx"], g["dWg"].to(Wg.dtype), g["dW1"].to(W1.dtype), g["dW3"].to(W3.dtype), g["dW2"].to(W2.dtype),
-                None, None)
+        grads = (g["dx"], g["dWg"].to(Wg.dtype), g["dW1"].to(W1.dtype), g["dW3"].to(W3.dtype), g["dW2"].to(W2.dtype))
+        if torch.is_grad_enabled():   # create_graph: the gradients are functions of all of these
+            grads = FirstDerivatives.apply(len(grads), *grads, x, Wg, W1, W3, W2, dout)
+        return (*grads, None, None)
+
+
+class FirstDerivatives(torch.autograd.Function):
+    """The layer's gradients beside what they are functions of: a derivative of them is not built, and raises
+    instead of being left out of a sum."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tensors[:n]
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("second derivatives of the MoE layer are not supported")
 
 
 class SparseMoE(torch.nn.Module):

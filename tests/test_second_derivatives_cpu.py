@@ -1,5 +1,5 @@
-"""Second derivatives through the grouped product's autograd functions are right, and not dropped.  The kernels are
-replaced by torch products: no GPU needed."""
+"""Second derivatives through the grouped product's autograd functions are right, those of the layer raise; neither
+are dropped.  The kernels are replaced by torch products: no GPU needed."""
 import pytest
 import torch
 
@@ -54,3 +54,25 @@ def test_grouped_linear(products, second):
         assert torch.allclose(g, w, rtol=1e-4, atol=1e-5)
 
 
+
+
+def test_layer(monkeypatch):
+    def forward(x, *weights, path, workspace):
+        return x * 2
+
+    def backward(x, Wg, W1, W3, W2, dout, k, ws, alpha, wgrad_dtype):
+        return dict(dx=dout * 2, dWg=torch.zeros_like(Wg), dW1=torch.zeros_like(W1), dW3=torch.zeros_like(W3),
+                    dW2=torch.zeros_like(W2)), 0
+
+    monkeypatch.setattr(nn, "moe_forward_ws", forward)
+    monkeypatch.setattr(nn, "moe_backward_ws", backward)
+    layer = nn.SparseMoE(8, 16, E=4, k=2, dtype=torch.float32, device="cpu")
+    x = torch.randn(3, 8, requires_grad=True)
+    dx, = torch.autograd.grad(layer(x).sum(), x, create_graph=True)
+    assert torch.equal(dx, torch.full_like(x, 2))
+    with pytest.raises(RuntimeError, match="second derivatives"):
+        (dx.pow(2).sum() + x.sum()).backward()
+    # the first derivatives with a graph that nobody follows
+    out = layer(x)
+    out.sum().backward(create_graph=True)
+    assert torch.equal(x.grad.detach(), torch.full_like(x, 2)) and layer.W1.grad is not None
