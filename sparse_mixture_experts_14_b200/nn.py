@@ -168,12 +168,27 @@ class GroupedLinear(torch.nn.Module):
         return GroupedMmFunction.apply(x.contiguous(), self.W, offsets, counts)
 
 
+def _contiguous_alike(g):
+    """The elements of g in the order of its memory where they fill it (a transposed gradient does), else a copy."""
+    if g.is_contiguous():
+        return g
+    v = g.permute(sorted(range(g.dim()), key=g.stride, reverse=True))
+    return v if v.is_contiguous() else g.contiguous()
+
+
+@torch.no_grad()
 def clip_grad_norm_(parameters, max_norm: float, eps: float = 1e-6):
     """Clip the gradients of the parameters (one, or an iterable) in place by their global 2-norm; returns
-    the norm before clipping (float32 [1], on the device).  No host synchronisation."""
+    the norm before clipping (float32 [1], on the parameters' device).  No host synchronisation."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
+    parameters = list(parameters)
     grads = [p.grad for p in parameters if p.grad is not None]
     if not grads:
-        return torch.zeros(1)
-    return moe_clip_grads(grads, max_norm, eps=eps)[0]
+        return torch.zeros(1, device=parameters[0].device if parameters else None)
+    flat = [_contiguous_alike(g) for g in grads]
+    norm = moe_clip_grads(flat, max_norm, eps=eps)[0]
+    for g, f in zip(grads, flat):
+        if f.data_ptr() != g.data_ptr():
+            g.copy_(f)
+    return norm

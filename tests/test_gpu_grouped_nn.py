@@ -125,3 +125,34 @@ def test_second_derivatives(mods):
     for g, w in ((gx, wx), (gW, wW)):
         assert (g.double() - w).abs().max() <= 5 * 118 * 2.0 ** -23 * 11 * w.abs().max()
     assert moe.moe_get_device_status() == moe.MOE_OK
+
+
+def test_clip_grad_norm_without_gradients(mods):
+    moe, nn = mods
+    p = torch.nn.Parameter(torch.ones(3, device="cuda"))
+    norm = nn.clip_grad_norm_([p], 1.0)
+    assert norm.device == p.device and norm.dtype == torch.float32 and norm.item() == 0.0
+    assert nn.clip_grad_norm_(iter([]), 1.0).item() == 0.0
+
+
+def test_clip_grad_norm_of_gradients_of_any_strides(mods):
+    """Transposed and permuted gradients, one with gaps between its rows, one of stride 2: as torch's clip."""
+    moe, nn = mods
+    torch.manual_seed(8)
+    grads = [torch.randn(6, 10, device="cuda").t(), torch.randn(3, 4, 5, device="cuda").permute(2, 0, 1),
+             torch.randn(7, 16, device="cuda")[:, :9], torch.randn(22, device="cuda").bfloat16()[::2],
+             torch.randn(5, device="cuda"), torch.randn(1, 4, device="cuda").expand(1, 4), torch.randn((), device="cuda")]
+    gaps = grads[2]._base[:, 9:].clone()
+    params = [torch.nn.Parameter(torch.zeros_like(g)) for g in grads]
+    for p, g in zip(params, grads):
+        p.grad = g
+    keep = [g.clone() for g in grads]
+    want = sum(k.double().pow(2).sum().item() for k in keep) ** 0.5
+    norm = nn.clip_grad_norm_(params, want / 3)
+    assert abs(norm.item() - want) <= 18 * 2.0 ** -24 * want
+    for p, g, k in zip(params, grads, keep):
+        assert p.grad is g
+        w = k.double() * (want / 3 / (want + 1e-6))
+        tol = 19 * 2.0 ** -24 + (2.0 ** -8 if g.dtype == torch.bfloat16 else 0)
+        assert ((g.double() - w).abs() <= tol * w.abs()).all()
+    assert torch.equal(grads[2]._base[:, 9:], gaps)
