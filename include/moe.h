@@ -591,8 +591,12 @@ MOE_API moe_status moe_grouped_lora(const void* x, const void* W, const int32_t*
  * c = 1); else out[i] has grads[i]'s length and type, and may be grads[i]
  * itself but no output may overlap another tensor.  norm [1] float (device,
  * out): n.  Squares are summed in fp64 over fp32 sums of at most 32, in a fixed
- * order (bitwise repeatable).  A NaN in any gradient makes n and every output
- * NaN; an infinite n gives c = 0.  0 <= max_norm <= Inf, 0 <= eps < Inf.
+ * order (bitwise repeatable), and c follows from the fp64 n: finite gradients
+ * whose n is above the float range (norm is then Inf) are still scaled to
+ * max_norm.  A NaN in any gradient makes n and every output NaN.  An Inf makes n
+ * Inf and, below max_norm = Inf, c 0 (zero times the Inf itself is NaN);
+ * max_norm = Inf leaves the values as they are.  0 <= max_norm <= Inf,
+ * 0 <= eps < Inf.
  * Scratch comes from the library's stream-ordered pool.
  * ------------------------------------------------------------------------ */
 typedef struct {

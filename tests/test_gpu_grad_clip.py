@@ -257,3 +257,48 @@ def test_outputs_by_name_and_by_shape(moe):
         moe.moe_clip_grads([g["dW1"]], 1.0, out=[torch.zeros(2, 6, 4)])                                # on the CPU
     with pytest.raises(moe.MoEError):
         moe.moe_clip_grads([g["dW1"]], 1.0, out=[torch.zeros(2, 6, 4, device="cuda").bfloat16()])      # another type
+
+
+@pytest.mark.parametrize("value,max_norm", [(1e38, 1e-3), (1e38, 1e-6), (3e38, 1.0), (2e30, 1e-12), (1e38, 1e-30),
+                                            (1e-20, 1e-30)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_factors_below_the_normal_range(moe, value, max_norm, dtype):
+    """c = max_norm / n may be below fp32's normal range while c g is in it; n may be above fp32's range.  Values
+    of all lengths: vectors, their rests, and off 16-byte alignment."""
+    buf = torch.full((9001,), value, device="cuda").to(dtype)
+    grads = [buf[:5003].clone(), buf[1:4000], torch.tensor([value / 3, -value], device="cuda")]
+    keep = [g.clone() for g in grads]
+    norm, outs = moe.moe_clip_grads(grads, max_norm, eps=0.0, out=[torch.empty_like(g) for g in grads])
+    n = _norm64(keep)
+    if n > 3.4028234e38:
+        assert norm.item() == float("inf")
+    c = min(1.0, torch.tensor(max_norm).double().item() / n)   # (max_norm travels as a float)
+    for o, g in zip(outs, keep):
+        # as _check_scaled; a result below the normal range is rounded to a multiple of the type's smallest, twice
+        # (the product, then the output)
+        tiny = 2.0 ** -149 if o.dtype == torch.float32 else 2.0 ** -133
+        tol = 19 * 2.0 ** -24 + (torch.finfo(torch.bfloat16).eps / 2 if o.dtype == torch.bfloat16 else 0)
+        want = g.double() * c
+        assert ((o.double() - want).abs() <= tol * want.abs() + tiny).all()
+
+
+def test_infinite_max_norm_leaves_infinite_gradients(moe):
+    g = [torch.tensor([1.0, float("inf"), -3.0], device="cuda"), torch.ones(40, device="cuda").bfloat16()]
+    norm, outs = moe.moe_clip_grads(g, float("inf"), out=[torch.zeros_like(t) for t in g])
+    assert norm.item() == float("inf") and all(torch.equal(o, t) for o, t in zip(outs, g))
+    g[1][7] = float("nan")
+    norm, outs = moe.moe_clip_grads(g, float("inf"), out=outs)
+    assert norm.isnan().all() and all(o.isnan().all() for o in outs)
+
+
+def test_a_factor_just_below_a_power_of_two(moe):
+    """c = 2^-110 (1 - 2^-40) rounds to a power of two in fp32: in place it still scales."""
+    g = [torch.zeros(64, device="cuda")]
+    g[0][3] = 2.0 ** 100 * (1 + 2.0 ** -20)
+    want = g[0].double() * (2.0 ** -10 / (2.0 ** 100 * (1 + 2.0 ** -20)))
+    norm, _ = moe.moe_clip_grads(g, 2.0 ** -10, eps=0.0)
+    assert ((g[0].double() - want).abs() <= 19 * 2.0 ** -24 * want.abs()).all()
+    g = [torch.zeros(64, device="cuda")]
+    g[0][3] = 2.0 ** 100
+    moe.moe_clip_grads(g, 2.0 ** -10 * (1 - 2.0 ** -24), eps=0.0)
+    assert abs(g[0][3].item() - 2.0 ** -10) <= 19 * 2.0 ** -34
