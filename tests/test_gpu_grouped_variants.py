@@ -63,3 +63,54 @@ def test_few_rows_of_one_expert_with_adapters(moe, rows, out_dtype, pattern, R):
     out = _call(moe, [rows], a[0], a[1], False, out_dtype, *a[2:])
     assert moe.moe_get_device_status() == moe.MOE_OK
     _verify_lora(out, [rows], a[0], *a[2:])
+
+
+# How far a long sum of random terms may be off, RMS of the error over RMS of the result, in units of 2^-23.  An
+# addition of a term to a running sum s that rounds to nearest errs by ulp(s) / sqrt(12), on average over s's mantissa
+# 0.21 2^-23 |s| (RMS); one that truncates, as the tensor cores do, by half an ulp in one direction, 0.36 2^-23 |s|.
+# With |s| = sqrt(k) of k terms of unit size:
+#   rounded, one chain of n:            0.21 sqrt(n / 2)                                        (n = 14336: 17.8)
+#   truncated, 16 terms to an addition, m additions to an accumulator, accumulators added with rounding:
+#       0.36 (4 * 2/3 m^1.5) / sqrt(16 m) = 0.24 m, and the rounded additions of n / 16 m sums   (m = 32: 7.7)
+N_LONG = 14336
+TILE, FEW, SIMT, ADAPTERS = 8.0, 3.0, 18.0, 9.0   # m = 32; m = 8; one chain of them all; m = 32 and u's own sums
+
+
+def _rms_error(got, want):
+    return ((got.double() - want).pow(2).mean().sqrt() / want.pow(2).mean().sqrt()).item() * 2.0 ** 23
+
+
+@pytest.mark.parametrize("dtype,op,counts,N,limit", [
+    ("bf16", "mm", [2000, 1800], 2048, TILE), ("bf16", "mm", [200], 264, TILE), ("bf16", "mm", [3, 40, 300], 264, TILE),
+    ("bf16", "mm", [8], 1024, FEW), ("bf16", "mm", [24], 520, FEW), ("bf16", "mm", [5, 0, 7, 9], 520, FEW),
+    ("bf16", "dgrad", [900, 1100], 520, TILE), ("bf16", "wgrad", [N_LONG], 512, TILE),
+    ("bf16", "wgrad", [N_LONG, 100], 2048, TILE),
+    ("f32", "mm", [2000, 1800], 2048, SIMT), ("f32", "mm", [60], 512, SIMT), ("f32", "mm", [30, 30, 25, 9], 512, SIMT),
+    ("f32", "mm", [7], 512, SIMT), ("f32", "dgrad", [300], 520, SIMT), ("f32", "wgrad", [N_LONG], 1024, SIMT),
+], ids=str)
+def test_long_sums_in_fp32(moe, dtype, op, counts, N, limit):
+    """Reductions of 14336 into fp32: what blocked accumulators and split sums are for."""
+    K = 768 if op == "wgrad" else N_LONG
+    size = (N_LONG, N) if op == "dgrad" else (N, K)
+    out, starts, x, dy, W = _product(moe, op, counts, *size, (dtype, "f32"), 55)
+    for e, (s, n) in enumerate(zip(starts, counts)):
+        r = slice(s, s + n)
+        if n == 0 or (op == "wgrad" and n < N_LONG):
+            continue
+        a, b, got = {"mm": lambda: (x[r], W[e].t(), out[r]), "dgrad": lambda: (dy[r], W[e], out[r]),
+                     "wgrad": lambda: (dy[r].t(), x[r], out[e])}[op]()
+        err = _rms_error(got, a.double() @ b.double())
+        assert err <= limit, (e, err, limit)
+
+
+@pytest.mark.parametrize("counts,limit", [([2000], ADAPTERS), ([200], ADAPTERS), ([8], FEW + 1), ([30], FEW + 1)], ids=str)
+def test_long_sums_in_fp32_with_adapters(moe, counts, limit):
+    N, L, R = 520, 5, 64
+    starts, rows, x, W, A, B, scale, ids = _inputs(counts, N, N_LONG, L, R, "runs", 56)
+    out = _call(moe, counts, starts, rows, False, "f32", x, W, A, B, scale, ids)
+    want = x.double() @ W[0].double().t()
+    for a in range(L):
+        m = ids == a
+        want[m] += (x[m].double() @ A[a, 0].double().t() * scale[a].double()) @ B[a, 0].double().t()
+    err = _rms_error(out, want)
+    assert err <= limit, (err, limit)
