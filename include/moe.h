@@ -564,9 +564,10 @@ MOE_API moe_status moe_grouped_wgrad(const void* dy, const void* x, const int32_
  *   A [L][E][R][K], B [L][E][N][R] bf16, scale [L] float, adapter [M] int32
  *   (device): the row's adapter in [0, L), or -1 for none.  Rows of one adapter
  *   need not be neighbours.  E = 1 with offsets {0, M}: one shared projection.
- * With a bfloat16 output s_a A x is rounded once to bf16 (the second product's
- * operand type), with a float output it keeps fp32's digits; the sum of both
- * products is rounded once.  A NaN or Inf in an adapter reaches the
+ * With a bfloat16 output s_a A x is rounded once to bf16 where the tensor cores'
+ * tiles multiply it (the second product's operand type) and to 16 bits or
+ * more in batches of few rows; with a float output it keeps fp32's digits.  The
+ * sum of both products is rounded once.  A NaN or Inf in an adapter reaches the
  * rows of that adapter only (other rows may be summed in another order then,
  * and the call takes several times as long).
  * An id outside [-1, L) in a segment records

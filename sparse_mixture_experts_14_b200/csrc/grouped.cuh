@@ -125,9 +125,12 @@ __host__ __device__ inline ColumnTiles column_tiles(int n) {
 }
 
 // The adapters as the products' kernels see them.  u is a workspace buffer [M][terms][R16], R16 = R
-// rounded up to 16 (zeros behind R); rows without an adapter hold nothing.  For a bf16 output u is one bf16
-// value, rounded like the operand it becomes; beside an fp32 output that rounding (2^-8 of u) would be the
-// largest error by far, so there u is the sum of three bf16 values, which hold fp32's 24 bits.
+// rounded up to 16 (zeros behind R); rows without an adapter hold nothing.  u is the sum of `terms` bf16 values:
+// three beside an fp32 output, which hold fp32's 24 bits (one alone, off by up to 2^-8 of u, would be the largest error by
+// far); for a bf16 output one where grouped_tc multiplies it, rounded like any of its operands, and two where
+// grouped_few alone does, on the CUDA cores.  (Two in grouped_tc: error 1.81e-3 -> 1.66e-3 of the result, which is
+// the output's own rounding, but 205 rows of 40 adapters of rank 32 take 47.1 us instead of 40.7, 4096 rows of 12 of
+// rank 64 549 instead of 508; in grouped_few, 32 rows, 167.8 and 167.4.)
 struct LoraView {
     const __nv_bfloat16* B;        // [L][E][N][R]
     const int32_t* adapter;        // [M]
@@ -135,7 +138,7 @@ struct LoraView {
     int32_t* tile_list;            // [column tiles][256]: the adapters that occur in the tile, each once
     int32_t* tile_count;           // [column tiles]
     int L, R, R16;
-    int terms;                     // 1 or 3
+    int terms;                     // 1, 2 or 3
     int per;                       // 16-wide slices of an adapter's part of a row of u
     int box;                       // ranks of a box of B: the widest of 64, 32, 16 that divides R16
 };
@@ -174,22 +177,6 @@ inline size_t lora_u_bytes(int M, int R) { return align_up((size_t)M * 3 * ((R +
 inline size_t lora_workspace_bytes(int M, int E, int R) {
     return lora_u_bytes(M, R) + align_up(lora_tiles(M, E) * (kColumnTile + 1) * 4, 256);
 }
-inline LoraView lora_view(const GroupedArgs& a) {
-    LoraView v;
-    v.B = static_cast<const __nv_bfloat16*>(a.B);
-    v.adapter = a.adapter;
-    v.u = reinterpret_cast<__nv_bfloat16*>(a.ws);
-    v.tile_list = reinterpret_cast<int32_t*>(a.ws + lora_u_bytes(a.seg.M, a.R));
-    v.tile_count = v.tile_list + lora_tiles(a.seg.M, a.seg.E) * kColumnTile;
-    v.L = a.L;
-    v.R = a.R;
-    v.R16 = (a.R + 15) / 16 * 16;
-    v.terms = a.out16 ? 1 : 3;
-    v.per = v.terms * v.R16 / 16;
-    v.box = v.R16 % 64 == 0 ? 64 : v.R16 % 32 == 0 ? 32 : 16;
-    return v;
-}
-
 cudaError_t launch_grouped_simt(const GroupedArgs& a, cudaStream_t s);   // float
 cudaError_t launch_grouped_tc(const GroupedArgs& a, cudaStream_t s);     // bfloat16, M > 0
 cudaError_t launch_grouped_few(const GroupedArgs& a, cudaStream_t s);    // bfloat16 mm with few rows
@@ -201,6 +188,21 @@ struct Choice {
     int limit;
 };
 Choice grouped_choice(const GroupedArgs& a);
+inline LoraView lora_view(const GroupedArgs& a) {
+    LoraView v;
+    v.B = static_cast<const __nv_bfloat16*>(a.B);
+    v.adapter = a.adapter;
+    v.u = reinterpret_cast<__nv_bfloat16*>(a.ws);
+    v.tile_list = reinterpret_cast<int32_t*>(a.ws + lora_u_bytes(a.seg.M, a.R));
+    v.tile_count = v.tile_list + lora_tiles(a.seg.M, a.seg.E) * kColumnTile;
+    v.L = a.L;
+    v.R = a.R;
+    v.R16 = (a.R + 15) / 16 * 16;
+    v.terms = !a.out16 ? 3 : grouped_choice(a).tc ? 1 : 2;
+    v.per = v.terms * v.R16 / 16;
+    v.box = v.R16 % 64 == 0 ? 64 : v.R16 % 32 == 0 ? 32 : 16;
+    return v;
+}
 cudaError_t launch_lora_shrink(const GroupedArgs& a, cudaStream_t s);    // u and the tiles' lists
 
 }  // namespace moe

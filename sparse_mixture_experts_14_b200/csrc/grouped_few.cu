@@ -51,7 +51,6 @@ __global__ void __launch_bounds__(32 * WARPS, 2) grouped_few_kernel(const FewPar
     constexpr int ROWS = 8 * NT;
     constexpr int U = 4;                   // steps whose loads are in flight together
     constexpr int PITCH = FEATURES + 1;
-    constexpr int TERMS = OUT16 ? 1 : 3;
     __shared__ SegTable seg;
     __shared__ float red[WARPS][ROWS][PITCH];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -166,7 +165,12 @@ __global__ void __launch_bounds__(32 * WARPS, 2) grouped_few_kernel(const FewPar
         for (int v = 0; v < WARPS; ++v) s += red[v][r][fl];
         if (LORA) {
             const int id = p.lora.adapter[row0 + r];
-            if (id >= 0 && id < p.lora.L) s += adapter_term<TERMS>(p.lora, (size_t)id * p.seg.E + e, N, row0 + r, f);
+            if (id >= 0 && id < p.lora.L) {
+                const size_t ae = (size_t)id * p.seg.E + e;
+                if (!OUT16) s += adapter_term<3>(p.lora, ae, N, row0 + r, f);
+                else s += p.lora.terms == 2 ? adapter_term<2>(p.lora, ae, N, row0 + r, f)
+                                            : adapter_term<1>(p.lora, ae, N, row0 + r, f);
+            }
         }
         const size_t at = (row0 + r) * N + f;
         if (OUT16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(s);

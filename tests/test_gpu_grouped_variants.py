@@ -114,3 +114,21 @@ def test_long_sums_in_fp32_with_adapters(moe, counts, limit):
         want[m] += (x[m].double() @ A[a, 0].double().t() * scale[a].double()) @ B[a, 0].double().t()
     err = _rms_error(out, want)
     assert err <= limit, (err, limit)
+
+
+@pytest.mark.parametrize("counts", [[2, 0, 5, 1], [29]], ids=str)
+@pytest.mark.parametrize("R", [8, 64])
+def test_few_rows_with_adapters_are_rounded_once(moe, counts, R):
+    """bf16 outputs of batches of few rows: s A x keeps 16 bits, so the output's own rounding is all there is.  RMS
+    errors: the rounding alone is about 1.7e-3 of the result; u is off by 2^-16 and the fp32 sums by 1e-6 at most,
+    which add a ten-thousandth to it (u in one bf16 value: a tenth)."""
+    N, K, L = 520, 1032, 4
+    starts, rows, x, W, A, B, scale, ids = _inputs(counts, N, K, L, R, "each", 57)
+    out = _call(moe, counts, starts, rows, False, "bf16", x, W, A, B, scale, ids)
+    want = torch.zeros(rows, N, dtype=torch.float64, device="cuda")
+    for e, (s, n) in enumerate(zip(starts, counts)):
+        for r in range(s, s + n):
+            a, xr = int(ids[r]), x[r].double()
+            want[r] = W[e].double() @ xr + B[a, e].double() @ (scale[a].double() * (A[a, e].double() @ xr))
+    rms = lambda t: t.double().pow(2).mean().sqrt().item()
+    assert rms(out.double() - want) <= 1.001 * rms(want.bfloat16().double() - want)
