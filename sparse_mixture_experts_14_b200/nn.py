@@ -26,6 +26,13 @@ from . import (MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_PATH_TRAIN, moe_backward_ws, m
                moe_forward_ws, moe_grouped_dgrad, moe_grouped_mm, moe_grouped_wgrad, moe_train_workspace_size)
 
 
+def _operand(t):
+    """t as the kernels take it: contiguous and 16-byte aligned.  A gradient may be a view at any offset of a
+    larger one, as that of a tensor that was flattened into a concatenation."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class MoEFunction(torch.autograd.Function):
     """out = MoE(x) with weights (Wg, W1, W3, W2); gradients for x and every weight.
 
@@ -48,7 +55,7 @@ class MoEFunction(torch.autograd.Function):
     def backward(ctx, dout):
         x, Wg, W1, W3, W2 = ctx.saved_tensors
         wd = torch.bfloat16 if W1.dtype == torch.bfloat16 else torch.float32
-        g, _ = moe_backward_ws(x, Wg, W1, W3, W2, dout.contiguous(), ctx.k, ctx.ws, alpha=ctx.alpha, wgrad_dtype=wd)
+        g, _ = moe_backward_ws(x, Wg, W1, W3, W2, _operand(dout), ctx.k, ctx.ws, alpha=ctx.alpha, wgrad_dtype=wd)
         ctx.ws = None
         grads = (g["dx"], g["dWg"].to(Wg.dtype), g["dW1"].to(W1.dtype), g["dW3"].to(W3.dtype), g["dW2"].to(W2.dtype))
         if torch.is_grad_enabled():   # create_graph: the gradients are functions of all of these
@@ -85,7 +92,7 @@ class SparseMoE(torch.nn.Module):
 
     def forward(self, x):
         shape = x.shape
-        x2 = x.reshape(-1, shape[-1]).contiguous()
+        x2 = _operand(x.reshape(-1, shape[-1]))
         weights = (self.Wg, self.W1, self.W3, self.W2)
         if torch.is_grad_enabled() and (x2.requires_grad or any(w.requires_grad for w in weights)):
             out = MoEFunction.apply(x2, *weights, self.k, self.alpha)
@@ -111,7 +118,7 @@ class GroupedMmFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         x, W, offsets, counts = ctx.saved_tensors
-        dy = dy.contiguous()
+        dy = _operand(dy)
         dx = dW = None
         if ctx.needs_input_grad[0]:
             dx = GroupedDgradFunction.apply(dy, W, offsets, counts)
@@ -133,7 +140,7 @@ class GroupedDgradFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         dy, W, offsets, counts = ctx.saved_tensors
-        g = g.contiguous()
+        g = _operand(g)
         ddy = GroupedMmFunction.apply(g, W, offsets, counts) if ctx.needs_input_grad[0] else None
         dW = GroupedWgradFunction.apply(dy, g, offsets, counts) if ctx.needs_input_grad[1] else None
         return ddy, dW, None, None
@@ -150,7 +157,7 @@ class GroupedWgradFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         dy, x, offsets, counts = ctx.saved_tensors
-        g = g.contiguous()
+        g = _operand(g)
         ddy = GroupedMmFunction.apply(x, g, offsets, counts) if ctx.needs_input_grad[0] else None
         dx = GroupedDgradFunction.apply(dy, g, offsets, counts) if ctx.needs_input_grad[1] else None
         return ddy, dx, None, None
@@ -165,7 +172,7 @@ class GroupedLinear(torch.nn.Module):
                                     math.sqrt(in_features))
 
     def forward(self, x, offsets, counts=None):
-        return GroupedMmFunction.apply(x.contiguous(), self.W, offsets, counts)
+        return GroupedMmFunction.apply(_operand(x), self.W, offsets, counts)
 
 
 def _contiguous_alike(g):

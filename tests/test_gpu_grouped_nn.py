@@ -156,3 +156,39 @@ def test_clip_grad_norm_of_gradients_of_any_strides(mods):
         tol = 19 * 2.0 ** -24 + (2.0 ** -8 if g.dtype == torch.bfloat16 else 0)
         assert ((g.double() - w).abs() <= tol * w.abs()).all()
     assert torch.equal(grads[2]._base[:, 9:], gaps)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_off_alignment(mods, dtype):
+    """The output goes into a concatenation behind one value: its gradient is contiguous at an odd offset; so is x."""
+    moe, nn = mods
+    torch.manual_seed(9)
+    off = torch.tensor([0, 20, 31], dtype=torch.int32, device="cuda")
+    lin = nn.GroupedLinear(2, 64, 40, dtype=DT[dtype])
+    x = torch.randn(1 + 31 * 64, device="cuda").to(DT[dtype])[1:].view(31, 64).requires_grad_()
+    dz = torch.randn(1 + 31 * 40, device="cuda").to(DT[dtype])
+    y = lin(x, off)
+    torch.cat([torch.zeros(1, device="cuda", dtype=DT[dtype]), y.flatten()]).backward(dz)
+    dy = dz[1:].view(31, 40)
+    for e, r in enumerate((slice(0, 20), slice(20, 31))):
+        W = lin.W.detach()[e]
+        check(y.detach()[r], *mm(x.detach()[r], W.t()), 64, "y")
+        check(x.grad[r], *mm(dy[r], W), 40, "dx")
+        check(lin.W.grad[e], *mm(dy[r].t(), x.detach()[r]), dy[r].shape[0], "dW")
+    layer = nn.SparseMoE(d=128, ffn=256, E=8, k=2)
+    h = torch.randn(1 + 16 * 128, device="cuda").bfloat16()
+    a = layer(h[1:].view(16, 128))
+    assert torch.equal(a, layer(h[1:].view(16, 128).clone()))
+    torch.cat([h[:1], a.flatten()]).sum().backward()
+    assert torch.isfinite(layer.W1.grad).all()
+    assert moe.moe_get_device_status() == moe.MOE_OK
+
+
+def test_empty_batch(mods):
+    moe, nn = mods
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    lin = nn.GroupedLinear(3, 64, 40)
+    x = torch.zeros(0, 64, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    y = lin(x, off)
+    y.sum().backward()
+    assert y.shape == (0, 40) and x.grad.shape == (0, 64) and (lin.W.grad == 0).all()
