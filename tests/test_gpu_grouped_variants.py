@@ -132,3 +132,21 @@ def test_few_rows_with_adapters_are_rounded_once(moe, counts, R):
             want[r] = W[e].double() @ xr + B[a, e].double() @ (scale[a].double() * (A[a, e].double() @ xr))
     rms = lambda t: t.double().pow(2).mean().sqrt().item()
     assert rms(out.double() - want) <= 1.001 * rms(want.bfloat16().double() - want)
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("per", [1, 20])
+def test_adapters_of_256_experts(moe, out_dtype, per):
+    counts = [per if e % 3 else 0 for e in range(256)]
+    a = _inputs(counts, 72, 136, 3, 8, "random", 58, lead=1, tail=2)
+    out = _call(moe, counts, a[0], a[1], True, out_dtype, *a[2:])
+    assert moe.moe_get_device_status() == moe.MOE_OK
+    _verify_lora(out, counts, a[0], *a[2:])
+
+
+def test_adapters_of_an_empty_batch(moe):
+    bf = lambda *shape: torch.zeros(*shape, dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    out = moe.moe_grouped_lora(bf(0, 64), bf(2, 40, 64), off, bf(4, 2, 8, 64), bf(4, 2, 40, 8),
+                               torch.ones(4, device="cuda"), off[:0])
+    assert out.shape == (0, 40) and moe.moe_get_device_status() == moe.MOE_OK
