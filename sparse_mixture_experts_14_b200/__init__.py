@@ -13,7 +13,8 @@ The block form adds h [T][d] (the residual stream, in place of x) and
 gamma [d]; load-balance statistics come back as a float32 [2E+1] tensor
 (f, p, loss).  The grouped products (moe_grouped_*) take the experts' weights on
 their own, with rows in any segments; moe_grad_norm and moe_clip_grads take the
-gradients of the backward calls.
+gradients of the backward calls.  None of these functions is recorded by autograd, whatever
+its tensors require: nn.py has the differentiable forms.
 """
 from __future__ import annotations
 

@@ -13,7 +13,12 @@
 //
 // Measured: 6296 rows of 7 experts, 1416 x 1264, 0.57 ms (0.67 with a product to an instruction); 1003 rows
 // of 5, 79 us; weight gradients of 8192 rows, 4 experts of 2048 x 1024, 0.68 ms (51 TFLOP/s; 0.92 with one).
-// What bounds it is the multiply-adds, and the last wave of blocks where it is not full.
+// What bounds it is the multiply-adds (73 % of the FMA pipe), and the last wave of blocks where it is not full.  One
+// or two experts are one or two library products, which are ahead there (mm of 96 rows, 4096 x 2048, 103 us against
+// 56; dgrad of 128 rows, 12032 x 104, 175 against 72): few tiles of 128 columns, and at most 8 parts of the reduction.
+//
+// Every output's part of the reduction is one chain of rounded additions: RMS error 7.6e-7 to 1.1e-6 of the result at a
+// reduction of 14336, where the library's fp32 product has 2.1e-6.
 //
 // Operands lie in shared memory with the reduction outermost.  Those that are read along
 // the reduction are turned on the way in; in the low tiles, where the weights' way into

@@ -52,9 +52,12 @@
 // the rest of that slice in shared memory, in both operands, before the MMA may
 // read it.
 //
-// Measured (8192 rows of 8 experts, 14336 x 4096, in a loop under the power cap, 1.3 GHz): mm 784 us, 1227 TFLOP/s,
-// dgrad 791, wgrad to bf16 817, to fp32 1130; cuBLAS on one dense matrix of the size 726.  Wide tiles are bound by
-// power there, narrow ones by the operands' way through shared memory.
+// Measured (8192 rows of 8 experts, 14336 x 4096, loops of 2 s at the 1000 W cap; us, and the SM clock in GHz that the
+// cap leaves): mm 765 (1.29), 1257 TFLOP/s; dgrad 794 (1.35); wgrad 814 (1.35); to fp32, on narrow tiles, 920 (1.44),
+// 887 (1.40) and 1131 (1.52).  cuBLAS on one dense matrix of the size: 731 (1.47).  Wide tiles do the most per clock (0.80
+// of the tensor cores' rate in mm) and run at the lowest one: power binds them.  Narrow ones wait for operands on their way
+// through shared memory (0.67), wgrad's to fp32 also for its epilogue (0.46: 16 blocks of the reduction to a tile of
+// 256 KB; the same tiles to bf16 992 us at the same clock).
 #include <cuda.h>
 
 #include "grouped.cuh"
@@ -209,10 +212,9 @@ __device__ __forceinline__ bool not_finite(uint32_t bits) { return (bits & 0x7f8
 // adapter, u_r B_{a,e}^T[f].  One warp, the 16 features from f0 on and n <= 32 rows, row0 and every step-th behind.
 // What another request's B does to a feature (zero times an infinity or NaN) it does to all of the tile's rows, so
 // a block in which every feature has a finite output is left as it is.  Products as in grouped_few.cu, operands
-// straight from global memory, 32 of the reduction in the tensor cores at a time and the rest with rounding.
-// (All outputs hit: 1500 rows of one expert,
-// 2048 x 2048, 43 -> 314 us; 4096 rows of 8, 14336 x 4096, 0.46 -> 5.3 ms, bound by L2.  One lane an output took 32 ms
-// for the first, inside the pipeline, whose waits are bounded.)
+// straight from global memory, 32 of the reduction in the tensor cores at a time and the rest with rounding.  (All
+// outputs hit: 1500 rows of one expert, 2048 x 2048, 43 -> 314 us; 4096 rows of 8, 14336 x 4096, 0.46 -> 5.3 ms, bound by
+// L2.  One lane an output took 32 ms for the first, inside the pipeline, whose waits are bounded.)
 __device__ __noinline__ void repair(const Params& p, int e, size_t row0, int n, int step, int f0) {
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int F = p.F, K = p.red;
@@ -897,9 +899,9 @@ __global__ void __launch_bounds__(Cfg<OP, OUT16, W, LORA, SPLIT>::THREADS, 1)
 }
 
 // Wide tiles (512 features) move a quarter fewer operand bytes per MMA through shared memory, which
-// bounds the narrow ones (8192 rows of 8 experts, 14336 x 4096, us narrow and wide: mm 796, 709; dgrad 892, 697;
-// wgrad to bf16 988, 745; 1024 rows 231, 229), but have one accumulator: for outputs of at least two waves of them,
-// and where they waste no more than an eighth of the features.
+// bounds the narrow ones (8192 rows of 8 experts, 14336 x 4096, us narrow and wide in loops of 2 s: mm 854, 765; dgrad 848,
+// 794; wgrad to bf16 992, 814; 1024 rows 231, 229), but have one accumulator: for outputs of at least two waves of
+// them, and where they waste no more than an eighth of the features.
 bool wide(const Params& p, long long cols, int pairs) {
     const long long nf = (p.F + 511) / 512;
     return cols * nf >= 2LL * pairs && nf * 512 * 8 <= (long long)p.F * 9;
